@@ -10,13 +10,19 @@ from .binding import (  # noqa: F401
     FlashAttention,
     attention_bwd,
     attention_bwd_varlen,
+    attention_chunk_paged,
     attention_decode_paged,
     attention_fwd,
     attention_fwd_fp8,
     attention_fwd_varlen,
     bwd_into,
     bwd_stages,
+    cache_read_paged,
+    cache_read_paged_into,
+    cache_write_paged,
     check,
+    chunk_paged_into,
+    chunk_workspace_bytes,
     decode_paged_into,
     decode_splits,
     decode_workspace_bytes,

@@ -20,7 +20,7 @@ FA_OK = 0
 STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
                 4: "FA_ERR_TIMEOUT", 5: "FA_ERR_NO_MEMORY", 6: "FA_ERR_DEVICE"}
 EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_varlen", "fa_fwd_fp8", "fa_decode_splits", "fa_decode_workspace_bytes", "fa_decode_paged",
-           "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_ex", "fa_bwd_varlen", "fa_bwd_deterministic", "fa_bwd_preprocess",
+           "fa_cache_write", "fa_cache_read", "fa_chunk_workspace_bytes", "fa_chunk_paged", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_ex", "fa_bwd_varlen", "fa_bwd_deterministic", "fa_bwd_preprocess",
            "fa_bwd_main", "fa_bwd_dq_convert", "fa_bwd_static_workspace", "fa_check", "fa_status_string")
 
 _lib = None
@@ -59,6 +59,13 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.fa_decode_workspace_bytes.restype = sz
     lib.fa_decode_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, i, i, i, vp, sz,
                                     vp]
+    ll = ctypes.c_longlong
+    lib.fa_cache_write.argtypes = [vp, vp, ll, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp]
+    lib.fa_cache_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, ll, i, i, i, i, i, i, i, vp]
+    lib.fa_chunk_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.fa_chunk_workspace_bytes.restype = sz
+    lib.fa_chunk_paged.argtypes = [vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, i, i, i, vp, sz,
+                                   vp]
     lib.fa_bwd_workspace_bytes.argtypes = [i, i, i, i]
     lib.fa_bwd_workspace_bytes.restype = sz
     lib.fa_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i, i, vp, sz, vp]
@@ -71,7 +78,7 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_bwd_static_workspace.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i, i, vp]
     for name in ("fa_fwd", "fa_fwd_ex", "fa_bwd_ex", "fa_fwd_varlen", "fa_bwd_varlen", "fa_fwd_fp8", "fa_decode_paged",
-                 "fa_bwd", "fa_bwd_deterministic", "fa_bwd_preprocess", "fa_bwd_main", "fa_bwd_dq_convert",
+                 "fa_cache_write", "fa_cache_read", "fa_chunk_paged", "fa_bwd", "fa_bwd_deterministic", "fa_bwd_preprocess", "fa_bwd_main", "fa_bwd_dq_convert",
                  "fa_bwd_static_workspace", "fa_check"):
         getattr(lib, name).restype = i
     return lib
@@ -421,3 +428,167 @@ def attention_bwd_varlen(q, k, v, o, lse, do, cu_seqlens, scale=None, causal=Fal
                               _stream_handle(stream))
     _raise(st, "fa_bwd_varlen")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- paged caches: ragged chunks
+
+
+def _on_device(t: torch.Tensor):
+    """Context that makes the tensor's device current (the C layer launches on the current device)."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device (there is no CPU path)")
+    return torch.cuda.device(t.device)
+
+
+def _check_rows(t: torch.Tensor, name: str, heads: int | None = None, d: int | None = None) -> int:
+    """Packed rows (total, heads, d) bf16, each row contiguous and 16-byte aligned; the rows may be slices of
+    a wider tensor. Returns the elements from one row to the next."""
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{name} must be a (total, heads, head_dim) bfloat16 CUDA tensor")
+    total, h, dim = t.shape
+    if (heads is not None and h != heads) or (d is not None and dim != d):
+        raise ValueError(f"{name} must be (total, {heads}, {d}) (got {tuple(t.shape)})")
+    s0, s1, s2 = t.stride()
+    if total <= 1:
+        s0 = h * dim
+    if (s2 != 1 and dim > 1) or (s1 != dim and h > 1) or s0 < h * dim or s0 % 8 or t.data_ptr() % 16:
+        raise ValueError(f"the rows of {name} must be contiguous, 16-byte aligned and a multiple of 8 elements apart")
+    return s0
+
+
+def _check_cache(like: torch.Tensor, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens):
+    """Pages, scales, block table, lengths and offsets of a ragged batch; returns (B, H, d, num_pages,
+    page_size, max_pages, k_scale pointer, v_scale pointer)."""
+    quantised = k_scale is not None
+    if quantised != (v_scale is not None):
+        raise ValueError("give both k_scale and v_scale (E4M3 pages), or neither (bfloat16 pages)")
+    kinds = (torch.float8_e4m3fn, torch.uint8) if quantised else (torch.bfloat16,)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must be (num_pages, page_size, heads, head_dim), of equal shape")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype not in kinds or not t.is_contiguous() or t.device != like.device:
+            raise ValueError(f"{name} must be contiguous, on the rows' device and {' or '.join(map(str, kinds))} "
+                             f"({'with' if quantised else 'without'} scales)")
+    num_pages, page_size, H, d = k_cache.shape
+    if quantised:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or not t.is_contiguous() or \
+                    t.device != like.device or tuple(t.shape) != (num_pages, H, page_size):
+                raise ValueError(f"{name} must be a contiguous (num_pages, heads, page_size) tensor of E8M0 bytes "
+                                 "(uint8 or float8_e8m0fnu) on the rows' device")
+    for t, name in ((block_table, "block_table"), (seqlens, "seqlens"), (cu_seqlens, "cu_seqlens")):
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != like.device:
+            raise ValueError(f"{name} must be a contiguous int32 tensor on the rows' device")
+    B = seqlens.numel()
+    if seqlens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B or \
+            tuple(cu_seqlens.shape) != (B + 1,):
+        raise ValueError("block_table must be (B, max_pages), seqlens (B,) and cu_seqlens (B + 1,)")
+    return (B, H, d, num_pages, page_size, block_table.shape[1], k_scale.data_ptr() if quantised else None,
+            v_scale.data_ptr() if quantised else None)
+
+
+def cache_write_paged(k_new, v_new, k_cache, v_cache, block_table, seqlens, cu_seqlens, k_scale=None, v_scale=None,
+                      stream=None) -> None:
+    """fa_cache_write: write the packed new rows k_new, v_new (total, H, d) bf16 into their pages, in place.
+    Sequence b's rows [cu_seqlens[b], cu_seqlens[b + 1]) are the last of its seqlens[b] positions; rows from
+    cu_seqlens[B] on are not read. k_cache, v_cache: (num_pages, page_size, H, d) bf16, or E4M3
+    (float8_e4m3fn or uint8) with k_scale, v_scale (num_pages, H, page_size) E8M0 bytes (uint8 or
+    float8_e8m0fnu): then each (token, head) row is quantised with its own power-of-two scale."""
+    with _on_device(k_new):
+        B, H, d, num_pages, page_size, max_pages, ks, vs = _check_cache(k_new, k_cache, v_cache, k_scale, v_scale,
+                                                                        block_table, seqlens, cu_seqlens)
+        stride = _check_rows(k_new, "k_new", H, d)
+        if v_new.shape != k_new.shape or v_new.device != k_new.device or _check_rows(v_new, "v_new", H, d) != stride:
+            raise ValueError("v_new must have the shape, device and row stride of k_new")
+        st = load().fa_cache_write(k_new.data_ptr(), v_new.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(),
+                                   ks, vs, block_table.data_ptr(), seqlens.data_ptr(), cu_seqlens.data_ptr(), B,
+                                   k_new.shape[0], H, d, num_pages, page_size, max_pages, _stream_handle(stream))
+        _raise(st, "fa_cache_write")
+
+
+def cache_read_paged_into(k_cache, v_cache, block_table, seqlens, cu_seqlens, k, v, k_scale=None, v_scale=None,
+                          stream=None) -> None:
+    """fa_cache_read: read the rows that cache_write_paged would write back into k, v (total, H, d) bf16,
+    exactly; rows from cu_seqlens[B] on are left as they were."""
+    with _on_device(k):
+        B, H, d, num_pages, page_size, max_pages, ks, vs = _check_cache(k, k_cache, v_cache, k_scale, v_scale,
+                                                                        block_table, seqlens, cu_seqlens)
+        stride = _check_rows(k, "k", H, d)
+        if v.shape != k.shape or v.device != k.device or _check_rows(v, "v", H, d) != stride:
+            raise ValueError("v must have the shape, device and row stride of k")
+        st = load().fa_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(),
+                                  seqlens.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), stride, B,
+                                  k.shape[0], H, d, num_pages, page_size, max_pages, _stream_handle(stream))
+        _raise(st, "fa_cache_read")
+
+
+def cache_read_paged(k_cache, v_cache, block_table, seqlens, cu_seqlens, total, k_scale=None, v_scale=None,
+                     stream=None):
+    """cache_read_paged_into new tensors: returns (k, v), (total, H, d) bf16 (rows from cu_seqlens[B] on,
+    if total is larger, are not initialised)."""
+    H, d = k_cache.shape[2:]
+    k, v = (_empty(stream, (total, H, d), torch.bfloat16, k_cache.device) for _ in range(2))
+    cache_read_paged_into(k_cache, v_cache, block_table, seqlens, cu_seqlens, k, v, k_scale, v_scale, stream)
+    return k, v
+
+
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    """A new tensor that a kernel on `stream` (None: the current one) may use until it is done."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and t.is_cuda:
+        t.record_stream(stream)
+    return t
+
+
+def chunk_workspace_bytes(B: int, total: int, Hq: int, Hkv: int, d: int) -> int:
+    """Bytes of workspace chunk_paged_into uses on the current device."""
+    return int(load().fa_chunk_workspace_bytes(B, total, Hq, Hkv, d))
+
+
+def chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, lse, scale=None, causal=False,
+                     window=(-1, -1), sinks=0, k_scale=None, v_scale=None, workspace=None, stream=None) -> None:
+    """fa_chunk_paged into caller-provided o (total, Hq, d) bf16 and lse (Hq, total) float32; rows from
+    cu_seqlens[B] on are left as they were. Arguments as attention_chunk_paged; ``workspace``: a uint8 CUDA
+    tensor of chunk_workspace_bytes(B, total, Hq, Hkv, d) bytes (any contents; calls that may overlap need
+    workspaces of their own), or None to allocate one."""
+    with _on_device(q):
+        B, Hkv, d, num_pages, page_size, max_pages, ks, vs = _check_cache(q, k_cache, v_cache, k_scale, v_scale,
+                                                                          block_table, seqlens, cu_seqlens)
+        stride = _check_rows(q, "q", None, d)
+        total, Hq, _ = q.shape
+        if o.shape != q.shape or o.dtype != torch.bfloat16 or o.device != q.device or not o.is_contiguous():
+            raise ValueError("o must be a contiguous bfloat16 tensor of q's shape on its device")
+        _check_lse(lse, (Hq, total))
+        if lse.device != q.device:
+            raise ValueError("lse must be on q's device")
+        if Hq == 0 or Hq % Hkv:
+            raise ValueError(f"the {Hq} query heads must be a multiple of the cache's {Hkv}")
+        if workspace is None:
+            own = torch.empty(chunk_workspace_bytes(B, total, Hq, Hkv, d), dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                own.record_stream(stream)
+            ws, wb = own.data_ptr(), own.numel()
+        else:
+            ws, wb = _check_workspace(workspace)
+        st = load().fa_chunk_paged(q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
+                                   block_table.data_ptr(), seqlens.data_ptr(), cu_seqlens.data_ptr(), o.data_ptr(),
+                                   lse.data_ptr(), B, total, Hq, Hkv, d, num_pages, page_size, max_pages,
+                                   _scale(scale, d), int(bool(causal)), int(window[0]), int(window[1]), int(sinks),
+                                   ws, wb, _stream_handle(stream))
+        _raise(st, "fa_chunk_paged")
+
+
+def attention_chunk_paged(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, scale=None, causal=False,
+                          window=(-1, -1), sinks=0, k_scale=None, v_scale=None, stream=None):
+    """Attention of ragged chunks of new tokens over a paged cache that holds their keys and values already
+    (cache_write_paged): returns (o, lse), o (total, Hq, d) bf16 and lse (Hq, total) float32.
+
+    q: (total, Hq, d) bf16, sequence b's rows [cu_seqlens[b], cu_seqlens[b + 1]) at the last positions of its
+    seqlens[b] keys; query head h reads cache head h // (Hq // Hkv). Pages and scales as in cache_write_paged.
+    ``window``: (left, right) as everywhere; ``sinks``: a sequence's first keys that stay visible left of the
+    window. Rows from cu_seqlens[B] on are not initialised (chunk_paged_into leaves them as they were)."""
+    o = _empty(stream, q.shape, torch.bfloat16, q.device)
+    lse = _empty(stream, (q.shape[1], q.shape[0]), torch.float32, q.device)
+    chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, lse, scale, causal, window, sinks,
+                     k_scale, v_scale, None, stream)
+    return o, lse

@@ -16,6 +16,8 @@
 #include "fa_sm100.h"
 #include "fa_bwd.cuh"
 #include "fa_bwd_dq.cuh"
+#include "fa_cache.cuh"
+#include "fa_chunk.cuh"
 #include "fa_decode.cuh"
 #include "fa_fwd.cuh"
 
@@ -86,6 +88,18 @@ bool decode_attributes() {
   return true;
 }
 
+template <int D, bool kF8, int kTiles>
+bool chunk_attribute() {
+  return cudaFuncSetAttribute(fa::fa_chunk_kernel<D, kF8, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fa::ChunkCfg<D, kF8, kTiles>::kSmemBytes) == cudaSuccess;
+}
+
+template <int D>
+bool chunk_attributes() {
+  return chunk_attribute<D, false, 1>() && chunk_attribute<D, false, 2>() && chunk_attribute<D, true, 1>() &&
+         chunk_attribute<D, true, 2>();
+}
+
 int device_setup(int* dev_out, int* sm_count) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
@@ -101,7 +115,8 @@ int device_setup(int* dev_out, int* sm_count) {
     if (g_is_sm100[dev]) {
       if (cudaFuncSetAttribute(fa::fa_fwd_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                fa::FwdCfg<128, true>::kSmemBytes) != cudaSuccess ||
-          !decode_attributes<64>() || !decode_attributes<128>() ||
+          !decode_attributes<64>() || !decode_attributes<128>() || !chunk_attributes<64>() ||
+          !chunk_attributes<128>() ||
           !bwd_attributes<64>() || !bwd_attributes<128>())
         return FA_ERR_CUDA;
     }
@@ -507,6 +522,188 @@ int check_workspace(void* workspace, size_t bytes, const Shape& s) {
   return FA_OK;
 }
 
+
+// ---------------------------------------------------------------- paged caches: ragged chunks
+
+// Host checks shared by the calls on a ragged batch over a paged cache.
+int check_paged(int B, int total, int H, int d, int num_pages, int page_size, int max_pages, const void* k_cache,
+                const void* v_cache, const void* k_scale, const void* v_scale, const int* block_table,
+                const int* seqlens, const int* cu) {
+  if (B < 1 || total < 0 || H < 1 || num_pages < 1 || page_size < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+  // TMA strides and coordinates; positions, packed rows and head counts stay in int with room to spare
+  if ((double)num_pages * page_size * H * d * 2 >= 1099511627776.0 || (double)num_pages * H >= 2147483647.0 ||
+      (double)max_pages * page_size > 1073741824.0 || total > 1073741824 || (double)H * d > 1073741824.0)
+    return FA_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache || !block_table || !seqlens || !cu) return FA_ERR_INVALID_ARG;
+  if ((k_scale == nullptr) != (v_scale == nullptr)) return FA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
+      !aligned(block_table, 4) || !aligned(seqlens, 4) || !aligned(cu, 4))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+bool any_overlap(const Span& a, const Span* others, int count) {
+  for (int i = 0; i < count; ++i)
+    if (a.p && others[i].p && overlap(a.p, a.n, others[i].p, others[i].n)) return true;
+  return false;
+}
+
+// Bytes from the first to the last of `total` packed rows of `width` elements, `stride` apart.
+size_t rows_bytes(int total, size_t width, long long stride) {
+  return total < 1 ? 0 : ((size_t)(total - 1) * (size_t)stride + width) * 2;
+}
+
+template <bool kWrite>
+int launch_cache(const fa::CacheParams& p, int d, cudaStream_t stream) {
+  const long long units = (long long)p.total * p.parts, per_block = fa::kCacheThreads / 32;
+  const long long blocks = (units + per_block - 1) / per_block;
+  if (blocks >= 2147483647LL) return FA_ERR_INVALID_ARG;
+  const bool f8 = p.scale[0] != nullptr;
+  void (*kernel)(fa::CacheParams);
+  if (kWrite)
+    kernel = d == 64 ? (f8 ? fa::fa_cache_write_kernel<64, true> : fa::fa_cache_write_kernel<64, false>)
+                     : (f8 ? fa::fa_cache_write_kernel<128, true> : fa::fa_cache_write_kernel<128, false>);
+  else
+    kernel = d == 64 ? (f8 ? fa::fa_cache_read_kernel<64, true> : fa::fa_cache_read_kernel<64, false>)
+                     : (f8 ? fa::fa_cache_read_kernel<128, true> : fa::fa_cache_read_kernel<128, false>);
+  kernel<<<(unsigned)blocks, fa::kCacheThreads, 0, stream>>>(p);
+  return launch_status();
+}
+
+// Writing (kWrite) or reading the rows [cu[b], cu[b + 1]) of every sequence.
+template <bool kWrite>
+int cache_rows(void* k_rows, void* v_rows, long long row_stride, void* k_cache, void* v_cache, void* k_scale,
+               void* v_scale, const int* block_table, const int* seqlens, const int* cu, int B, int total, int H,
+               int d, int num_pages, int page_size, int max_pages, fa_stream_t stream) {
+  int st = check_paged(B, total, H, d, num_pages, page_size, max_pages, k_cache, v_cache, k_scale, v_scale,
+                       block_table, seqlens, cu);
+  if (st) return st;
+  if (total > 0 && (!k_rows || !v_rows)) return FA_ERR_INVALID_ARG;
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || row_stride < (long long)H * d || row_stride % 8 != 0 ||
+      row_stride > 1073741824LL)
+    return FA_ERR_INVALID_ARG;
+  const bool f8 = k_scale != nullptr;
+  const size_t rb = rows_bytes(total, (size_t)H * d, row_stride);
+  const size_t cells = (size_t)num_pages * page_size * H, cb = cells * d * (f8 ? 1 : 2);
+  const Span caches[4] = {{k_cache, cb}, {v_cache, cb}, {k_scale, cells}, {v_scale, cells}};
+  const Span rows[2] = {{k_rows, rb}, {v_rows, rb}};
+  const Span plan[3] = {{block_table, (size_t)B * max_pages * 4}, {seqlens, (size_t)B * 4}, {cu, (size_t)(B + 1) * 4}};
+  for (int i = 0; i < 4; ++i) {
+    if (any_overlap(caches[i], rows, 2) || any_overlap(caches[i], caches + i + 1, 3 - i)) return FA_ERR_INVALID_ARG;
+    if (kWrite && any_overlap(caches[i], plan, 3)) return FA_ERR_INVALID_ARG;
+  }
+  if (!kWrite && (any_overlap(rows[0], plan, 3) || any_overlap(rows[1], plan, 3))) return FA_ERR_INVALID_ARG;
+  // (K and V rows may be slices of one tensor: their spans interleave. Read back, they must not.)
+  if (!kWrite && total > 0 && row_stride == (long long)H * d && overlap(k_rows, rb, v_rows, rb))
+    return FA_ERR_INVALID_ARG;
+  int dev, sms;
+  if ((st = device_setup(&dev, &sms))) return st;
+  if (total == 0) return FA_OK;
+  fa::CacheParams p;
+  p.B = B;
+  p.total = total;
+  p.H = H;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.parts = (int)(((long long)H * d + fa::kCacheWarpElems - 1) / fa::kCacheWarpElems);
+  p.row_stride = row_stride;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.cu = cu;
+  p.rows[0] = k_rows;
+  p.rows[1] = v_rows;
+  p.cache[0] = k_cache;
+  p.cache[1] = v_cache;
+  p.scale[0] = static_cast<uint8_t*>(k_scale);
+  p.scale[1] = static_cast<uint8_t*>(v_scale);
+  return launch_cache<kWrite>(p, d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+               const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return FA_ERR_CUDA;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_INVALID_ARG;
+}
+
+// Queries (total, Hkv, G, d), rows q_stride elements apart: a box is 64 columns of tq tokens' G heads.
+int make_map_chunk_q(CUtensorMap* m, const void* q, int total, int Hkv, int G, int d, long long q_stride, int tq) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)Hkv, (cuuint64_t)total};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)G * d * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)tq};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Pages (num_pages, page_size, H, d): box_rows rows of one head, 64 bf16 columns (swizzled) or all
+// d codes of E4M3 pages (as they lie).
+int make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int H, int d, int box_rows,
+                   bool f8) {
+  const cuuint64_t e = f8 ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)page_size, (cuuint64_t)num_pages};
+  const cuuint64_t strides[3] = {d * e, (cuuint64_t)H * d * e, (cuuint64_t)page_size * H * d * e};
+  const cuuint32_t box[4] = {f8 ? (cuuint32_t)d : 64u, 1, (cuuint32_t)box_rows, 1};
+  return encode_map(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides,
+                    box, f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Scales (num_pages * H, page_size): box_rows consecutive keys of one head.
+int make_map_scales(CUtensorMap* m, const void* base, int num_pages, int page_size, int H, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)page_size, (cuuint64_t)num_pages * H};
+  const cuuint64_t strides[1] = {(cuuint64_t)page_size};
+  const cuuint32_t box[2] = {(cuuint32_t)box_rows, 1};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// One or two 128-row tiles per block of the chunk kernel: two share every K/V load, which long
+// chunks need; with at most one tile of rows per sequence on average the second would stand idle.
+int chunk_tiles(int B, int total, int G) { return (double)total * G <= 128.0 * B ? 1 : 2; }
+
+struct ChunkWorkspace {
+  size_t o_bytes, lse_bytes, count_bytes;
+  size_t bytes() const { return o_bytes + lse_bytes + count_bytes; }
+};
+ChunkWorkspace chunk_workspace(int pieces, int tiles, int d) {
+  const size_t rows = (size_t)2 * pieces * tiles * 128;  // two partial slots per piece
+  return {align256(rows * d * 4), align256(rows * 4), align256((size_t)pieces * 4)};
+}
+
+template <int D, bool kF8, int kTiles>
+int chunk_launch(int grid, const CUtensorMap* m, const fa::ChunkParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(fa::ChunkCfg<D, kF8, kTiles>::kThreads);
+  cfg.dynamicSmemBytes = fa::ChunkCfg<D, kF8, kTiles>::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fa::fa_chunk_kernel<D, kF8, kTiles>, m[0], m[1], m[2], m[3], m[4], p) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+template <int D>
+int chunk_variant(bool f8, int tiles, int grid, const CUtensorMap* m, const fa::ChunkParams& p, cudaStream_t stream) {
+  if (f8) return tiles == 1 ? chunk_launch<D, true, 1>(grid, m, p, stream) : chunk_launch<D, true, 2>(grid, m, p, stream);
+  return tiles == 1 ? chunk_launch<D, false, 1>(grid, m, p, stream) : chunk_launch<D, false, 2>(grid, m, p, stream);
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------- backward without allocation
@@ -812,6 +1009,126 @@ int fa_decode_paged(const void* q, void* k_cache, void* v_cache, const void* k_n
       st = launch_decode<128>(grid, mk, mv, p, cs);
   }
   if (wbytes > 0 && !workspace && cudaFreeAsync(ws, cs) != cudaSuccess && !st) st = FA_ERR_CUDA;
+  return st;
+}
+
+int fa_cache_write(const void* k_new, const void* v_new, long long row_stride, void* k_cache, void* v_cache,
+                   void* k_scale, void* v_scale, const int* block_table, const int* seqlens, const int* cu_seqlens,
+                   int B, int total, int H, int d, int num_pages, int page_size, int max_pages, fa_stream_t stream) {
+  return cache_rows<true>(const_cast<void*>(k_new), const_cast<void*>(v_new), row_stride, k_cache, v_cache, k_scale,
+                          v_scale, block_table, seqlens, cu_seqlens, B, total, H, d, num_pages, page_size, max_pages,
+                          stream);
+}
+
+int fa_cache_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                  const int* block_table, const int* seqlens, const int* cu_seqlens, void* k, void* v,
+                  long long row_stride, int B, int total, int H, int d, int num_pages, int page_size, int max_pages,
+                  fa_stream_t stream) {
+  return cache_rows<false>(k, v, row_stride, const_cast<void*>(k_cache), const_cast<void*>(v_cache),
+                           const_cast<void*>(k_scale), const_cast<void*>(v_scale), block_table, seqlens, cu_seqlens,
+                           B, total, H, d, num_pages, page_size, max_pages, stream);
+}
+
+size_t fa_chunk_workspace_bytes(int B, int total, int Hq, int Hkv, int d) {
+  if (B < 1 || total < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  int dev, sms;
+  if (device_setup(&dev, &sms)) return 0;
+  return chunk_workspace(sms, chunk_tiles(B, total, Hq / Hkv), d).bytes();
+}
+
+int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const void* k_scale,
+                   const void* v_scale, const int* block_table, const int* seqlens, const int* cu_seqlens, void* o,
+                   float* lse, int B, int total, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                   float scale, int causal, int win_l, int win_r, int sinks, void* workspace,
+                   size_t workspace_bytes_, fa_stream_t stream) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || win_l < -1 || win_r < -1 || sinks < 0 || !std::isfinite(scale))
+    return FA_ERR_INVALID_ARG;
+  int st = check_paged(B, total, Hkv, d, num_pages, page_size, max_pages, k_cache, v_cache, k_scale, v_scale,
+                       block_table, seqlens, cu_seqlens);
+  if (st) return st;
+  const int G = Hq / Hkv;
+  if (G > 128) return FA_ERR_UNSUPPORTED;
+  if (total > 0 && (!q || !o || !lse)) return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || q_stride < (long long)Hq * d || q_stride % 8 != 0 ||
+      q_stride > 1073741824LL || (double)total * Hq >= 1099511627776.0)
+    return FA_ERR_INVALID_ARG;
+  const bool f8 = k_scale != nullptr;
+  const int max_keys = max_pages * page_size;
+  if (causal) win_r = 0;
+  if (win_l >= max_keys) win_l = -1;
+  if (win_r >= max_keys) win_r = -1;
+  if (win_l < 0) sinks = 0;  // no left bound: every first key is visible anyway
+  const size_t cells = (size_t)num_pages * page_size * Hkv, cb = cells * d * (f8 ? 1 : 2);
+  const size_t ob = (size_t)total * Hq * d * 2, lb = (size_t)total * Hq * 4;
+  const Span ins[8] = {{q, rows_bytes(total, (size_t)Hq * d, q_stride)}, {k_cache, cb}, {v_cache, cb},
+                       {k_scale, cells}, {v_scale, cells}, {block_table, (size_t)B * max_pages * 4},
+                       {seqlens, (size_t)B * 4}, {cu_seqlens, (size_t)(B + 1) * 4}};
+  if (any_overlap({o, ob}, ins, 8) || any_overlap({lse, lb}, ins, 8) || (o && lse && overlap(o, ob, lse, lb)))
+    return FA_ERR_INVALID_ARG;
+  int dev, sms;
+  if ((st = device_setup(&dev, &sms))) return st;
+  if (total == 0) return FA_OK;
+  const int tiles = chunk_tiles(B, total, G), tq = 128 / G;
+  const ChunkWorkspace wb = chunk_workspace(sms, tiles, d);
+  if (workspace) {
+    const Span ws{workspace, wb.bytes()};
+    if (!aligned(workspace, 256) || workspace_bytes_ < wb.bytes() || any_overlap(ws, ins, 8) ||
+        overlap(workspace, ws.n, o, ob) || overlap(workspace, ws.n, lse, lb))
+      return FA_ERR_INVALID_ARG;
+  }
+  // pieces: one per SM, and no more than the key tiles there can be
+  const double blocks = (double)(total / (tiles * tq)) + std::min(B, total);
+  const double most = blocks * Hkv * ((max_keys + 127) / 128 + 1);
+  const int pieces = most < sms ? (int)most : sms;
+  int box_rows = 16;
+  while (box_rows < 128 && page_size % (2 * box_rows) == 0) box_rows *= 2;
+  CUtensorMap m[5];
+  if ((st = make_map_chunk_q(&m[0], q, total, Hkv, G, d, q_stride, tq)) ||
+      (st = make_map_pages(&m[1], k_cache, num_pages, page_size, Hkv, d, box_rows, f8)) ||
+      (st = make_map_pages(&m[2], v_cache, num_pages, page_size, Hkv, d, box_rows, f8)))
+    return st;
+  m[3] = m[1];
+  m[4] = m[2];
+  if (f8 && ((st = make_map_scales(&m[3], k_scale, num_pages, page_size, Hkv, box_rows)) ||
+             (st = make_map_scales(&m[4], v_scale, num_pages, page_size, Hkv, box_rows))))
+    return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  void* ws = workspace;
+  if (!ws && cudaMallocAsync(&ws, wb.bytes(), cs) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_NO_MEMORY;
+  }
+  fa::ChunkParams p;
+  p.B = B;
+  p.total = total;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.tq = tq;
+  p.page_size = page_size;
+  p.box_rows = box_rows;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.win_l = win_l;
+  p.win_r = win_r;
+  p.sinks = sinks;
+  p.pieces = pieces;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.cu = cu_seqlens;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.o_part = static_cast<float*>(ws);
+  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(ws) + wb.o_bytes);
+  p.arrivals = reinterpret_cast<int*>(static_cast<char*>(ws) + wb.o_bytes + wb.lse_bytes);
+  if (log_enabled())
+    std::fprintf(stderr, "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d pieces=%d box=%d win=(%d,%d) sinks=%d\n",
+                 B, total, Hq, Hkv, d, f8, tiles, pieces, box_rows, win_l, win_r, sinks);
+  fa::fa_decode_prep_kernel<<<1, 256, 0, cs>>>(p.arrivals, pieces);
+  st = launch_status();
+  if (!st) st = d == 64 ? chunk_variant<64>(f8, tiles, pieces, m, p, cs) : chunk_variant<128>(f8, tiles, pieces, m, p, cs);
+  if (!workspace && cudaFreeAsync(ws, cs) != cudaSuccess && !st) st = FA_ERR_CUDA;
   return st;
 }
 

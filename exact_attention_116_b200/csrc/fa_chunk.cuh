@@ -1,0 +1,861 @@
+// Attention of chunks of new tokens over a paged KV cache, for sm_100a.
+//
+// A batch of ragged chunks: sequence b holds n_b = seqlens[b] keys in its pages, and the packed
+// query rows [cu[b], cu[b + 1]) are its last new_b positions: row i sits at pos = n_b - new_b + i.
+// Query head h reads key/value head h / G (G = Hq / Hkv). For each of them
+//   O = softmax(scale * q . k_j) V over the visible keys,  LSE = ln sum_j exp(scale * q . k_j);
+// key j < n_b is visible when j <= pos + win_r (win_r = 0 under causal masking; -1: no bound) and
+// when j >= pos - win_l (-1: no bound) or j < sinks: a sliding window beside which the sequence's
+// first keys stay visible. A row that sees no key gets O = 0 and LSE = -inf.
+//
+// Rows of a tile: the G query heads of a key/value head share its keys, so a 128-row tile holds
+// tq = 128 / G consecutive tokens times their G heads (row = token * G + head), and a block of
+// work is kTiles such tiles that share every K/V load. Its keys are visited in 128-key tiles: the
+// sink tiles before the window, then the window's (all tiles without one).
+//
+// Work split: for each key/value head, the key tiles of all blocks are listed block after block;
+// the lists of all heads, one after another, are cut into P equal contiguous pieces, one per CTA
+// (one CTA per SM). So every CTA visits the same number of key tiles (within one), for decoding
+// steps, long prompts and mixtures alike. A block that lies in one piece is finished by its CTA;
+// otherwise each of its pieces writes a partial (O / l, log2 l + m) and the piece that arrives last
+// merges them by their log-sum-exp, in piece order (the same sum whichever arrives last).
+//
+// Both products run on the tensor core, with the forward's roles and order of issue: S_t(v + 1)
+// ahead of P V_t(v), a row's 128 scores split over two warps that exchange their maxima, P in
+// TMEM, O rescaled only when a row's maximum has grown by more than 2^8, O divided by the sum of
+// the rounded weights.
+//
+// E4M3 pages (kF8): the codes of a K or V tile and their power-of-two scales are loaded as they
+// are, and four warps write the tile's values, code * 2^e, as bf16 into the operand buffers: exact,
+// since a code has 4 significant bits. The products then are those of bf16 pages holding these
+// values; 8-bit products would have to round Q and P to 4 bits.
+#pragma once
+
+#include "fa_cache.cuh"
+#include "fa_decode.cuh"
+#include "fa_fwd.cuh"
+
+namespace fa {
+
+struct ChunkParams {
+  int B, total, Hq, Hkv, G;
+  int tq;          // tokens per 128-row tile: 128 / G
+  int page_size;
+  int box_rows;    // rows of one page box: the largest power of two that divides page_size, <= 128
+  int max_pages, num_pages;
+  float scale_log2;  // scale * log2(e)
+  int win_l, win_r;  // -1 = unbounded; causal already folded into win_r = 0
+  int sinks;         // first keys that stay visible left of the window
+  int pieces;        // P
+  const int* block_table;  // (B, max_pages)
+  const int* seqlens;      // (B)
+  const int* cu;           // (B + 1)
+  __nv_bfloat16* o;        // (total, Hq, d)
+  float* lse;              // (Hq, total), natural log
+  float* o_part;           // (2 P, kTiles * 128, d) fp32
+  float* lse_part;         // (2 P, kTiles * 128), log2 domain
+  int* arrivals;           // (P) pieces of the block that starts in piece r and goes on, finished
+};
+
+template <int D, bool kF8, int kTiles>
+struct ChunkCfg {
+  static constexpr int kSoftWarps = 8 * kTiles;       // row split: two warps per 32 rows
+  static constexpr int kSoftThreads = 32 * kSoftWarps;
+  static constexpr int kConvThreads = kF8 ? 128 : 0;
+  static constexpr int kThreads = 128 + kSoftThreads + kConvThreads;
+  static constexpr int kBoxes = D / 64;               // 128-byte boxes per bf16 row
+  static constexpr int kTileBytes = 128 * D * 2;      // a bf16 tile of Q, K or V
+  static constexpr int kRawBytes = 128 * D;           // the codes of a K or V tile
+  static constexpr int kRawSlotBytes = kRawBytes + 1024;  // codes, then the scales of each page box at 128 bytes
+  static constexpr int kSlots = kF8 ? (D == 64 ? 6 : kTiles == 2 ? 3 : 4) : (D == 64 ? 10 : kTiles == 2 ? 4 : 5);
+  static constexpr int kRawSlots = kF8 ? (D == 64 ? 6 : 3) : 0;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKV = kTiles * kTileBytes;
+  static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
+  static constexpr int kOffX = kOffRaw + kRawSlots * kRawSlotBytes;
+  static constexpr int kXBytes = 4096 * kTiles;       // per tile: maxima [parity][half][row], sums [sum][half][row]
+  static constexpr int kOffBar = kOffX + kXBytes;
+  static constexpr int kSmemBytes = kOffBar + 1024 + 1024;  // barriers + alignment slack
+  static constexpr bool kShareS = kTiles == 2 && D == 128;  // one S buffer for both tiles
+  static constexpr uint32_t kColS0 = 0, kColS1 = kShareS ? 0 : 128;
+  static constexpr uint32_t kColP0 = kShareS ? 128 : 384, kColP1 = kShareS ? 192 : 448;
+  static constexpr uint32_t kColO0 = 256, kColO1 = 256 + D;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+};
+
+template <class Cfg>
+struct ChunkBars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[Cfg::kSlots], kv_empty[Cfg::kSlots];
+  uint64_t raw_full[Cfg::kRawSlots + 1], raw_empty[Cfg::kRawSlots + 1];
+  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int last_flag;            // merge: this piece arrived last
+  int first_b, first_blk;   // the piece's first block
+  long long first_start;    // its position on the head's list
+  long long sums[32];       // scans
+};
+
+// A sequence: first packed row, rows and keys. Offsets or lengths out of range make it empty
+// (reported by report_bad_batch).
+struct ChunkSeq {
+  int c0, rows, n;
+};
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b) {
+  ChunkSeq s;
+  s.c0 = __ldg(p.cu + b);
+  const int c1 = __ldg(p.cu + b + 1), n = __ldg(p.seqlens + b);
+  s.rows = (s.c0 < 0 || c1 < s.c0 || c1 > p.total) ? 0 : c1 - s.c0;
+  s.n = (n < 0 || n > (long long)p.max_pages * p.page_size) ? 0 : n;
+  return s;
+}
+
+// Keys visible to some row of a block, and the tiles that hold them: tile v of the block is key
+// tile v for v < ns (sinks left of the window), lo + v - ns from there on; cnt >= 1 in all (a
+// block that sees nothing visits one tile with every key masked).
+struct ChunkKeys {
+  int vis_lo, vis_hi;  // window part (vis_hi < 0: nothing visible)
+  int ns, lo, cnt;
+  __device__ __forceinline__ int tile(int v) const { return v < ns ? v : lo + v - ns; }
+};
+__device__ __forceinline__ ChunkKeys chunk_keys(const ChunkParams& p, int n, int pos0, int pos1) {
+  ChunkKeys k;
+  k.vis_lo = p.win_l >= 0 ? max(0, pos0 - p.win_l) : 0;
+  k.vis_hi = p.win_r >= 0 ? (int)min((long long)n - 1, (long long)pos1 + p.win_r) : n - 1;
+  k.ns = 0;
+  k.lo = 0;
+  k.cnt = 1;
+  if (pos1 < 0 || k.vis_hi < 0) {
+    k.vis_hi = -1;
+    return k;
+  }
+  k.lo = min(k.vis_lo, k.vis_hi) >> 7;
+  k.ns = min((int)(((long long)min(p.sinks, n) + 127) >> 7), k.lo);
+  k.cnt = k.ns + (k.vis_hi >> 7) - k.lo + 1;
+  return k;
+}
+
+// A walk over the blocks of one piece. A block: head h, sequence b, tokens [i0, i0 + ntok) of its
+// chunk; its tiles [v0, v1) belong to the piece.
+template <int kTiles>
+struct ChunkWalk {
+  long long u0, u1, th;  // the piece's range of the list of all heads, the length of one head's list
+  int h, b, blk;
+  ChunkSeq s;
+  ChunkKeys keys;
+  long long start;  // position of the block's first tile on the list of all heads
+  int i0, ntok, v0, v1;
+
+  __device__ __forceinline__ void set(const ChunkParams& p) {
+    const int tokens = kTiles * p.tq;
+    i0 = blk * tokens;
+    ntok = min(tokens, s.rows - i0);
+    const int pos0 = s.n - s.rows + i0;
+    keys = chunk_keys(p, s.n, pos0, pos0 + ntok - 1);
+    v0 = (int)max(0LL, u0 - start);
+    v1 = (int)min((long long)keys.cnt, u1 - start);
+  }
+  __device__ __forceinline__ bool valid() const { return start < u1; }
+  __device__ __forceinline__ void begin(const ChunkParams& p, int h_, int b_, int blk_, long long start_, long long u0_,
+                                        long long u1_, long long th_) {
+    u0 = u0_;
+    u1 = u1_;
+    th = th_;
+    h = h_;
+    b = b_;
+    blk = blk_;
+    start = start_;
+    if (!valid()) return;
+    s = chunk_seq(p, b);
+    set(p);
+  }
+  __device__ __forceinline__ void next(const ChunkParams& p) {
+    start += keys.cnt;
+    if (!valid()) return;
+    if (++blk * kTiles * p.tq >= s.rows) {
+      blk = 0;
+      do {
+        if (++b == p.B) {
+          b = 0;
+          ++h;
+        }
+        s = chunk_seq(p, b);
+      } while (s.rows == 0);
+    }
+    set(p);
+  }
+  __device__ __forceinline__ int pos0(int tq, int t) const { return s.n - s.rows + i0 + t * tq; }
+};
+
+// Inclusive scan over the block's threads of non-negative counts; scratch holds 32 values.
+__device__ __forceinline__ long long block_scan(long long x, long long* scratch, long long& total) {
+  const int warp = threadIdx.x >> 5, lane = lane_id(), warps = blockDim.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += v;
+  }
+  __syncthreads();  // the scratch of an earlier scan has been read
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  total = 0;
+  long long before = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  return x + before;
+}
+
+// E4M3 codes, four in a word, to bf16 values times f (two packed factors per row: f, and g for
+// scales whose exponent does not fit one factor). A code's exponent and mantissa bits, shifted
+// into a bf16's, are the value times 2^-120 (subnormals included); f makes up for it.
+__device__ __forceinline__ uint32_t e4m3_pair_bits(uint32_t spread) {  // bytes at bits 8..15 and 24..31
+  return ((spread >> 4) & 0x07f007f0u) | (spread & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two-dimensional tiled load (the scales of E4M3 pages).
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Row maximum of kC scores with the window and the sinks masked: key kbase + cc is visible when
+// it lies in [kmin, kmax] or is one of the first `sinks` keys and at most kmax.
+template <int kC>
+__device__ __forceinline__ void chunk_mask(float (&x)[kC], int kbase, int kmin, int kmax, int sinks) {
+  const bool any = kmax >= kmin;
+  const unsigned span = any ? (unsigned)(kmax - kmin) : 0u;
+  const int off = any ? kbase - kmin : -(1 << 30);
+  if (kbase < sinks) {
+    const int lim = min(sinks - 1, kmax) - kbase;
+#pragma unroll
+    for (int cc = 0; cc < kC; ++cc) x[cc] = ((unsigned)(off + cc) <= span || cc <= lim) ? x[cc] : -INFINITY;
+  } else {
+#pragma unroll
+    for (int cc = 0; cc < kC; ++cc) x[cc] = ((unsigned)(off + cc) <= span) ? x[cc] : -INFINITY;
+  }
+}
+
+template <int D, bool kF8, int kTiles>
+__global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
+    fa_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKs,
+                    const __grid_constant__ CUtensorMap tmVs, const ChunkParams p) {
+  using Cfg = ChunkCfg<D, kF8, kTiles>;
+  using Bars = ChunkBars<Cfg>;
+  using Walk = ChunkWalk<kTiles>;
+  static_assert(sizeof(Bars) <= 1024, "barrier block");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
+  const uint32_t smem_end = smem_u32(smem_raw) + Cfg::kSmemBytes;  // for the FA_DEBUG bounds checks
+  Bars* bars = reinterpret_cast<Bars*>(smem_gen + Cfg::kOffBar);
+  auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
+  const Abort ab{&bars->abort_flag};
+  const long long max_keys = (long long)p.max_pages * p.page_size;
+
+  if (tid == 0) {
+    bars->abort_flag = 0;
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(bars->q_full[t]), 1);
+      mbar_init(bar(bars->q_empty[t]), 1);
+      mbar_init(bar(bars->s_full[t]), 1);
+      mbar_init(bar(bars->s_empty[t]), 256);
+      mbar_init(bar(bars->p_full[t]), 256);
+      mbar_init(bar(bars->pv_done[t]), 1);
+    }
+    for (int s = 0; s < Cfg::kSlots; ++s) {
+      mbar_init(bar(bars->kv_full[s]), kF8 ? 4 : 1);  // one arrival per converting warp, or the loads'
+      mbar_init(bar(bars->kv_empty[s]), 1);
+    }
+    for (int s = 0; s < Cfg::kRawSlots; ++s) {
+      mbar_init(bar(bars->raw_full[s]), 1);
+      mbar_init(bar(bars->raw_empty[s]), 4);
+    }
+    mbar_init(bar(bars->mma_done), 1);
+    fence_barrier_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars->tmem_base), Cfg::kTmemCols);
+    tmem_relinquish();
+    tc_fence_before_sync();
+  }
+
+  // ---- the piece of this CTA: blocks per run of sequences, then key tiles per run of blocks
+  long long u0, u1, th;
+  {
+    if (blockIdx.x == 0) report_bad_batch(p.cu, p.seqlens, p.B, p.total, max_keys);
+    const int nthr = Cfg::kThreads, tokens = kTiles * p.tq;
+    int* run_base = reinterpret_cast<int*>(smem_gen);  // [kThreads], over the Q buffer (no load is in flight yet)
+    const int run = (p.B + nthr - 1) / nthr;
+    const int rb0 = min(p.B, tid * run), rb1 = min(p.B, rb0 + run);
+    long long blocks = 0;
+    for (int b = rb0; b < rb1; ++b) blocks += (chunk_seq(p, b).rows + tokens - 1) / tokens;
+    long long nb;
+    const long long blocks_incl = block_scan(blocks, bars->sums, nb);
+    run_base[tid] = (int)(blocks_incl - blocks);
+    __syncthreads();
+    // this thread's blocks [q0, q1): found by the run of sequences that holds q0
+    const long long q0 = nb * tid / nthr, q1 = nb * (tid + 1) / nthr;
+    int b = 0, blk = 0;
+    long long tiles = 0;
+    if (q0 < q1) {
+      int lo = 0, hi = nthr - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (run_base[mid] <= q0) lo = mid;
+        else hi = mid - 1;
+      }
+      b = lo * run;
+      blk = (int)(q0 - run_base[lo]);
+    }
+    // visit the thread's blocks in order; f(b, blk, tiles of the block) until it returns false
+    auto visit = [&](auto f) {
+      int bb = b, kk = blk;
+      for (long long q = q0; q < q1;) {
+        const ChunkSeq s = chunk_seq(p, bb);
+        const int nbb = (s.rows + tokens - 1) / tokens;
+        if (kk >= nbb) {
+          kk -= nbb;
+          ++bb;
+          continue;
+        }
+        const int i0 = kk * tokens, pos0 = s.n - s.rows + i0;
+        if (!f(bb, kk, chunk_keys(p, s.n, pos0, pos0 + min(tokens, s.rows - i0) - 1).cnt)) return;
+        ++kk;
+        ++q;
+      }
+    };
+    visit([&](int, int, int cnt) {
+      tiles += cnt;
+      return true;
+    });
+    const long long tiles_incl = block_scan(tiles, bars->sums, th);
+    const long long T = th * p.Hkv;
+    const int pe = (int)min((long long)p.pieces, T);
+    const int r = blockIdx.x;
+    u0 = r < pe ? dec_piece_lo(T, pe, r) : T;
+    u1 = r < pe ? dec_piece_lo(T, pe, r + 1) : T;
+    const long long w0 = th > 0 ? u0 % th : 0, excl = tiles_incl - tiles;
+    if (u0 < u1 && excl <= w0 && w0 < tiles_incl) {
+      long long at = excl;
+      visit([&](int bb, int kk, int cnt) {
+        if (w0 >= at + cnt) {
+          at += cnt;
+          return true;
+        }
+        bars->first_b = bb;
+        bars->first_blk = kk;
+        bars->first_start = at;
+        return false;
+      });
+    }
+    fence_proxy_async_smem();  // run_base has been read: the Q loads may overwrite it
+  }
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  const uint32_t sKV = smem_base + Cfg::kOffKV, sRaw = smem_base + Cfg::kOffRaw;
+  auto sQ = [&](int t) { return smem_base + Cfg::kOffQ + t * Cfg::kTileBytes; };
+  const int h0 = th > 0 ? (int)(u0 / th) : 0;
+  auto begin = [&](Walk& w) {
+    if (u0 < u1)
+      w.begin(p, h0, bars->first_b, bars->first_blk, bars->first_start + (long long)h0 * th, u0, u1, th);
+    else
+      w.begin(p, 0, 0, 0, u1, u1, u1, th);
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer (all lanes)
+    // Lane l loads page box l % groups of 64-column box l / groups (E4M3: lanes from 16 on the
+    // scales of a box). Boxes of keys that no row of the block sees are filled with zeros by a
+    // coordinate past the pool: their page entries are not read.
+    const int groups = 128 / p.box_rows;
+    const int grp = (kF8 ? lane & 15 : lane) % groups, col = (kF8 ? lane & 15 : lane) / groups;
+    const bool loads = col < (kF8 ? 1 : Cfg::kBoxes), scales = kF8 && lane >= 16;
+    const uint32_t box_off = (uint32_t)grp * p.box_rows;
+    uint32_t n = 0, qn[2] = {0, 0};  // K/V tiles issued, Q tiles issued
+    constexpr int kRing = kF8 ? Cfg::kRawSlots : Cfg::kSlots;
+    Walk w;
+    begin(w);
+    // page and row of this lane's box of tile v of block w; page num_pages: zeros
+    auto place = [&](const Walk& x, int v, int& page, int& row) {
+      const int key = x.keys.tile(v) * 128 + (int)box_off, last = key + p.box_rows - 1;
+      page = p.num_pages;
+      row = 0;
+      if (!loads || key > x.keys.vis_hi || (last < x.keys.vis_lo && key >= p.sinks)) return;
+      const long long ti = (long long)x.b * p.max_pages + key / p.page_size;
+      if (!dbg_range(ab, ti, 1, (long long)p.B * p.max_pages)) return;
+      page = __ldg(p.block_table + ti);
+      row = key % p.page_size;
+      if (page < 0 || page >= p.num_pages) {
+        atomicOr(&g_fa_error, kErrBadInput);
+        page = p.num_pages;
+      }
+    };
+    int page = 0, row = 0;
+    if (w.valid()) place(w, w.v0, page, row);
+    for (; w.valid() && !ab.raised();) {
+      const int nact = (kTiles == 2 && w.ntok > p.tq) ? 2 : 1;
+      if (lane == 0) {
+        for (int t = 0; t < nact; ++t) {
+          mbar_wait(bar(bars->q_empty[t]), (qn[t] & 1) ^ 1, ab);
+          const int tok = w.s.c0 + w.i0 + t * p.tq;
+          bool ok = true;
+          for (int bx = 0; bx < Cfg::kBoxes; ++bx)
+            ok = ok && dbg_tma(ab, bx * 64, 0, w.h, tok, D, p.G, p.Hkv, p.total, 2, sQ(t) + bx * 16384, 16384,
+                               smem_base, smem_end);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(bars->q_full[t]), (uint32_t)(p.tq * p.G * D * 2));
+#pragma unroll
+          for (int bx = 0; bx < Cfg::kBoxes; ++bx)
+            tma_load_4d(sQ(t) + bx * 16384, &tmQ, bar(bars->q_full[t]), bx * 64, 0, w.h, tok);
+          ++qn[t];
+        }
+      }
+      __syncwarp();
+      const int h = w.h;
+      for (int v = w.v0; v < w.v1 && !ab.raised(); ++v) {
+        const int pg = page, rw = row;
+        if (v + 1 < w.v1) place(w, v + 1, page, row);  // the next tile's page, read while this one waits
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const uint32_t slot = n % kRing, phase = (n / kRing) & 1;
+          uint64_t& full = kF8 ? bars->raw_full[slot] : bars->kv_full[slot];
+          mbar_wait(kF8 ? bar(bars->raw_empty[slot]) : bar(bars->kv_empty[slot]), phase ^ 1, ab);
+          if (FA_DEBUG) {  // (page num_pages, the zero fill, lies just past the pool)
+            const uint32_t to = kF8 ? sRaw + slot * Cfg::kRawSlotBytes + box_off * D
+                                    : sKV + slot * Cfg::kTileBytes + col * 16384 + box_off * 128;
+            const bool ok = !loads || dbg_tma(ab, kF8 ? 0 : col * 64, h, rw, pg, D, p.Hkv, p.page_size,
+                                              p.num_pages + 1, kF8 ? 1 : 2, to, p.box_rows * (kF8 ? D : 128),
+                                              smem_base, smem_end);
+            if (!__all_sync(0xffffffffu, ok)) break;
+          }
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar(full), kF8 ? (uint32_t)(Cfg::kRawBytes + 128) : (uint32_t)Cfg::kTileBytes);
+          __syncwarp();
+          if constexpr (kF8) {
+            const uint32_t base = sRaw + slot * Cfg::kRawSlotBytes;
+            if (loads && !scales)
+              tma_load_4d(base + box_off * D, kv ? &tmV : &tmK, bar(full), 0, h, rw, pg);
+            else if (loads)
+              tma_load_2d(base + Cfg::kRawBytes + grp * 128, kv ? &tmVs : &tmKs, bar(full), rw, pg * p.Hkv + h);
+          } else if (loads) {
+            tma_load_4d(sKV + slot * Cfg::kTileBytes + col * 16384 + box_off * 128, kv ? &tmV : &tmK, bar(full),
+                        col * 64, h, rw, pg);
+          }
+        }
+      }
+      w.next(p);
+      if (w.valid()) place(w, w.v0, page, row);
+    }
+    // every load issued lands before the CTA exits
+    for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
+      mbar_drain(kF8 ? bar(bars->raw_full[i % kRing]) : bar(bars->kv_full[i % kRing]), (i / kRing) & 1);
+    if (lane == 0)
+      for (int t = 0; t < 2; ++t)
+        if (qn[t] > 0) mbar_drain(bar(bars->q_full[t]), (qn[t] - 1) & 1);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (elect_one()) {
+      constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);  // S = Q K^T (both K-major)
+      constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);     // O += P V (V MN-major)
+      const uint32_t tS[2] = {tmem + Cfg::kColS0, tmem + Cfg::kColS1};
+      const uint32_t tO[2] = {tmem + Cfg::kColO0, tmem + Cfg::kColO1};
+      const uint32_t tP[2] = {tmem + Cfg::kColP0, tmem + Cfg::kColP1};
+      uint32_t kvn = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, sn[2] = {0, 0};
+      auto kv_wait = [&](uint32_t n) {
+        const uint32_t s = n % Cfg::kSlots;
+        mbar_wait(bar(bars->kv_full[s]), (n / Cfg::kSlots) & 1, ab);
+        tc_fence_after_sync();
+        return s;
+      };
+      auto issue_s = [&](int t, uint32_t ks, bool last) {  // once the S before it in the buffer has been read
+        const int buf = Cfg::kShareS ? 0 : t;
+        mbar_wait(bar(bars->s_empty[buf]), (sn[buf] & 1) ^ 1, ab);
+        ++sn[buf];
+        tc_fence_after_sync();
+        const uint32_t k_smem = sKV + ks * Cfg::kTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          mma_ss(tS[t], sdesc_kmajor(sQ(t) + off), sdesc_kmajor(k_smem + off), idS, kk > 0);
+        }
+        mma_commit(bar(bars->s_full[t]));
+        if (last) mma_commit(bar(bars->q_empty[t]));  // the block's last read of Q_t
+      };
+      auto issue_pv = [&](int t, uint32_t vs, bool first) {
+        mbar_wait(bar(bars->p_full[t]), pn[t] & 1, ab);
+        ++pn[t];
+        tc_fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tO[t], tP[t] + kk * 8, sdesc_mnmajor(sKV + vs * Cfg::kTileBytes + kk * 2048, 16384), idO,
+                 !first || kk > 0);
+        mma_commit(bar(bars->pv_done[t]));
+      };
+      Walk w;
+      for (begin(w); w.valid(); w.next(p)) {
+        const int nact = (kTiles == 2 && w.ntok > p.tq) ? 2 : 1, nv = w.v1 - w.v0;
+        for (int t = 0; t < nact; ++t) mbar_wait(bar(bars->q_full[t]), (qn[t]++) & 1, ab);
+        tc_fence_after_sync();
+        uint32_t ks = kv_wait(kvn);
+        for (int t = 0; t < nact; ++t) issue_s(t, ks, nv == 1);
+        mma_commit(bar(bars->kv_empty[ks]));
+        for (int v = 0; v < nv; ++v) {
+          const bool more = v + 1 < nv;
+          const uint32_t vs = kv_wait(kvn + 1);
+          kvn += 2;
+          if (more) ks = kv_wait(kvn);
+          for (int t = 0; t < nact; ++t) {
+            if (more) issue_s(t, ks, v + 2 == nv);
+            if (more && t == nact - 1) mma_commit(bar(bars->kv_empty[ks]));
+            issue_pv(t, vs, v == 0);
+          }
+          mma_commit(bar(bars->kv_empty[vs]));
+        }
+      }
+      mma_commit(bar(bars->mma_done));
+      mbar_drain(bar(bars->mma_done), 0);
+    }
+  } else if (warp >= 4 && warp < 4 + Cfg::kSoftWarps) {
+    // ---------------------------------------------------------------- softmax + epilogue
+    constexpr int kC = 64;                                    // scores of a row per thread and key tile
+    const int t = kTiles == 2 ? ((warp - 4) >> 2) & 1 : 0;    // tile of the block
+    const int half = (warp - 4) >> (kTiles == 2 ? 3 : 2);     // columns [64 half, 64 half + 64)
+    const int row = (tid - 128) & 127;                        // TMEM lane and row within the tile
+    const int st = tid - 128;                                 // index among the softmax threads
+    const uint32_t lane_field = (uint32_t)((row & ~31) << 16);
+    const uint32_t tS = tmem + lane_field + (t ? Cfg::kColS1 : Cfg::kColS0) + kC * half;
+    const uint32_t tO = tmem + lane_field + (t ? Cfg::kColO1 : Cfg::kColO0);
+    const uint32_t tP = tmem + lane_field + (t ? Cfg::kColP1 : Cfg::kColP0) + (kC / 2) * half;
+    float* xm = reinterpret_cast<float*>(smem_gen + Cfg::kOffX) + t * 1024;  // [parity][half][row]
+    float* xl = xm + 512;                                                    // [sum][half][row]
+    uint32_t sn = 0, pvn = 0, xu = 0, vn = 0;  // vn: key tiles of this CTA so far (K/V stream position 2 vn)
+    auto pair_sync = [&]() { named_bar_sync(4 + 4 * t + (row >> 5), 64); };
+    const float c = p.scale_log2;
+    const bool pos_scale = c > 0.0f;
+    const int tok_in_tile = row / p.G, head_in_group = row - tok_in_tile * p.G;
+
+    Walk w;
+    for (begin(w); w.valid(); w.next(p)) {
+      const int nv = w.v1 - w.v0;
+      const int tile_tok = min(p.tq, w.ntok - t * p.tq);  // tokens of this tile (<= 0: no such tile)
+      const int rows = tile_tok * p.G;                    // its rows
+      const bool act = tile_tok > 0, live = (row & ~31) < rows;  // (live: some row of this warp)
+      const int pos = w.pos0(p.tq, t) + tok_in_tile;
+      const bool mine = row < rows;
+      const int kmax = (!mine || pos < 0) ? -1
+                       : p.win_r >= 0     ? (int)min((long long)w.s.n - 1, (long long)pos + p.win_r)
+                                          : w.s.n - 1;
+      const int kmin = p.win_l >= 0 ? max(0, pos - p.win_l) : 0;
+      const int pos_lo = w.pos0(p.tq, t), pos_hi = pos_lo + tile_tok - 1;
+      float m_run = -INFINITY, l_run = 0.0f, lr_run = 0.0f;
+
+      for (int v = 0; act && v < nv; ++v) {
+        const int key0 = w.keys.tile(w.v0 + v) * 128;
+        mbar_wait(bar(bars->s_full[t]), sn & 1, ab);
+        ++sn;
+        tc_fence_after_sync();
+        if (!live) {  // no row of this warp: keep the barriers' counts
+          mbar_arrive(bar(bars->s_empty[Cfg::kShareS ? 0 : t]));
+          if (v > 0) {
+            mbar_wait(bar(bars->pv_done[t]), pvn & 1, ab);
+            ++pvn;
+          }
+          mbar_arrive(bar(bars->p_full[t]));
+          continue;
+        }
+        uint32_t r[kC / 32][32];
+#pragma unroll
+        for (int q4 = 0; q4 < kC / 32; ++q4) tmem_ld32(tS + q4 * 32, r[q4]);
+#pragma unroll
+        for (int q4 = 0; q4 < kC / 32; ++q4) tmem_wait_ld(r[q4]);
+        tc_fence_before_sync();  // the S buffer may now take the next scores
+        mbar_arrive(bar(bars->s_empty[Cfg::kShareS ? 0 : t]));
+        float x[kC];
+#pragma unroll
+        for (int cc = 0; cc < kC; ++cc) x[cc] = __uint_as_float(r[cc >> 5][cc & 31]);
+
+        const int k1 = key0 + 127, kbase = key0 + kC * half;
+        const bool all = pos_lo >= 0 && k1 < w.s.n && (p.win_r < 0 || k1 <= (long long)pos_lo + p.win_r) &&
+                         (p.win_l < 0 || key0 >= pos_hi - p.win_l || k1 < p.sinks);
+        if (!all) chunk_mask(x, kbase, kmin, kmax, p.sinks);
+        float m_tile = pos_scale ? fwd_tile_max<true>(x, false, 0, 0, 0, c) : -INFINITY;
+        if (!pos_scale) {
+          if (!all) {  // masked scores must stay -inf whatever the scale's sign
+#pragma unroll
+            for (int cc = 0; cc < kC; ++cc) x[cc] = x[cc] == -INFINITY ? -INFINITY : x[cc] * c;
+          } else {
+#pragma unroll
+            for (int cc = 0; cc < kC; ++cc) x[cc] *= c;
+          }
+          for (int cc = 0; cc < kC; ++cc) m_tile = fmaxf(m_tile, x[cc]);
+        }
+        {
+          float* slot = xm + (xu & 1) * 256;
+          slot[half * 128 + row] = m_tile;
+          pair_sync();
+          m_tile = fmaxf(m_tile, slot[(half ^ 1) * 128 + row]);
+          ++xu;
+        }
+        float alpha;
+        bool updated;
+        fwd_update_max(m_tile, m_run, alpha, updated);
+        const float m_use = (m_run == -INFINITY) ? 0.0f : m_run;
+        if (v > 0) {  // P V of the tile before has read P_t, and O_t is quiescent
+          mbar_wait(bar(bars->pv_done[t]), pvn & 1, ab);
+          ++pvn;
+          tc_fence_after_sync();
+        }
+        float2 sum = make_float2(0.0f, 0.0f), rsum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int q4 = 0; q4 < kC / 32; ++q4) {
+          uint32_t pk[16];
+          if (pos_scale)
+            fwd_exp_chunk<true>(x, q4 * 16, c, m_use, pk, sum, rsum);
+          else
+            fwd_exp_chunk<false>(x, q4 * 16, c, m_use, pk, sum, rsum);
+          tmem_st16(tP + q4 * 16, pk);
+        }
+        l_run = l_run * alpha + (sum.x + sum.y);
+        lr_run = lr_run * alpha + (rsum.x + rsum.y);
+        if (__any_sync(0xffffffffu, updated && v > 0)) {
+#pragma unroll 1
+          for (int cc = (D / 2) * half; cc < (D / 2) * (half + 1); cc += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + cc, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + cc, o);
+          }
+        }
+        if constexpr (!kF8) {
+          // V rows that no row of the block sees may hold anything, a NaN among it: 0 (their
+          // weights are 0). The live warps of each tile write the same zeros before their P V.
+          const int keys_end = w.keys.vis_hi - key0 + 1;  // rows from here on
+          const int win_from = w.keys.vis_lo - key0, sink_end = p.sinks - key0;  // and rows [sink_end, win_from)
+          if (keys_end < 128 || (win_from > 0 && sink_end < 128)) {
+            const uint32_t vi = 2 * (vn + v) + 1, vs = vi % Cfg::kSlots;
+            mbar_wait(bar(bars->kv_full[vs]), (vi / Cfg::kSlots) & 1, ab);
+            const int lw = min(4, (rows + 31) >> 5);  // live warps per half
+            const int li = (half * lw + ((row >> 5))) * 32 + lane, ln = 64 * lw;
+            for (int e = li; e < 128 * Cfg::kBoxes * 8; e += ln) {
+              const int vr = e / (Cfg::kBoxes * 8), rest = e % (Cfg::kBoxes * 8);
+              if (vr >= keys_end || (vr < win_from && vr >= sink_end))
+                st_shared_v4(sKV + vs * Cfg::kTileBytes + (rest >> 3) * 16384 + vr * 128 + (rest & 7) * 16, 0u, 0u, 0u,
+                             0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(bar(bars->p_full[t]));
+      }
+
+      // ---- epilogue: O / (sum of the weights applied) and the log-sum-exp, final or partial
+      const long long T = w.th * p.Hkv;
+      const int pe = (int)min((long long)p.pieces, T), piece = blockIdx.x;
+      const int pf = dec_piece_of(T, pe, w.start), pl = dec_piece_of(T, pe, w.start + w.keys.cnt - 1);
+      // slot of the block's partial in piece r: 2 r, or 2 r + 1 where an earlier block opens the piece
+      auto slot_of = [&](int r) { return 2 * r + (r == pf && dec_piece_lo(T, pe, pf) < w.start ? 1 : 0); };
+      if (act) {
+        mbar_wait(bar(bars->pv_done[t]), pvn & 1, ab);
+        ++pvn;
+        tc_fence_after_sync();
+      }
+      if (act && live) {
+        xl[half * 128 + row] = l_run;
+        xl[256 + half * 128 + row] = lr_run;
+        pair_sync();
+        const float l_tot = l_run + xl[(half ^ 1) * 128 + row];
+        const float l_o = lr_run + xl[256 + (half ^ 1) * 128 + row];
+        const float inv_l = l_o > 0.0f ? 1.0f / l_o : 0.0f;
+        const float lse2 = l_tot > 0.0f ? m_run + lg2_approx(l_tot) : (l_tot == l_tot ? -INFINITY : l_tot);
+        const bool dead = !(l_o > 0.0f) && l_o == l_o;  // no visible key (a NaN sum is not one)
+        const long long tok = (long long)w.s.c0 + w.i0 + t * p.tq + tok_in_tile;
+        const int head = w.h * p.G + head_in_group;
+        const long long prow = (long long)slot_of(piece) * (kTiles * 128) + t * 128 + row;
+        const long long o_size = (long long)p.total * p.Hq * D, part_size = 2LL * p.pieces * kTiles * 128 * D;
+#pragma unroll 1
+        for (int cc = (D / 2) * half; cc < (D / 2) * (half + 1); cc += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + cc, o);
+          tmem_wait_ld(o);
+          if (!mine) continue;
+          const float mul = l_o == l_o ? inv_l : l_o;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = dead ? 0u : __float_as_uint(__uint_as_float(o[e]) * mul);
+          if (pf == pl) {
+            const long long oi = (tok * p.Hq + head) * D + cc;
+            if (dbg_range(ab, oi, 32, o_size)) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint4 q;
+                q.x = pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+                q.y = pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                q.z = pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+                q.w = pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+                *reinterpret_cast<uint4*>(p.o + oi + e) = q;
+              }
+            }
+          } else if (dbg_range(ab, prow * D + cc, 32, part_size)) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(p.o_part + prow * D + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (mine && half == 0) {
+          const long long li = (long long)head * p.total + tok;
+          if (pf != pl) {
+            if (dbg_range(ab, prow, 1, part_size / D)) p.lse_part[prow] = lse2;
+          } else if (dbg_range(ab, li, 1, (long long)p.Hq * p.total)) {
+            p.lse[li] = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
+          }
+        }
+        tc_fence_before_sync();
+      }
+      vn += nv;
+
+      if (pf != pl) {
+        // ---- the block is spread over pieces pf..pl: the last one to arrive merges
+        __threadfence();  // this thread's partials are visible device-wide before the arrival
+        named_bar_sync(1, Cfg::kSoftThreads);
+        if (st == 0) {
+          griddep_wait();  // the arrival counters have been zeroed
+          const int before = dbg_range(ab, pf, 1, p.pieces) ? atomicAdd(&p.arrivals[pf], 1) : -1;
+          bars->last_flag = before == pl - pf;
+        }
+        named_bar_sync(1, Cfg::kSoftThreads);
+        if (bars->last_flag) {
+          __threadfence();
+          const int brows = w.ntok * p.G;  // rows of the block: tile 1's start at row 128 of a slot
+          for (int e = st; e < brows * (D / 4); e += Cfg::kSoftThreads) {
+            const int rr = e / (D / 4), c4 = (e - rr * (D / 4)) * 4;
+            const int itok = rr / p.G, g = rr - itok * p.G, tile = itok >= p.tq ? 1 : 0;
+            const int srow = tile * 128 + rr - tile * p.tq * p.G;
+            auto prow_of = [&](int r) { return (long long)slot_of(r) * (kTiles * 128) + srow; };
+            float mx = -INFINITY;
+            for (int r = pf; r <= pl; ++r) mx = fmaxf(mx, __ldcg(p.lse_part + prow_of(r)));
+            float wsum = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float m_sub = mx == -INFINITY ? 0.0f : mx;
+            for (int r = pf; r <= pl; ++r) {
+              const long long pr = prow_of(r);
+              const float wr = ex2_approx(__ldcg(p.lse_part + pr) - m_sub);
+              const float4 o4 = __ldcg(reinterpret_cast<const float4*>(p.o_part + pr * D + c4));
+              wsum += wr;
+              acc.x = fmaf(wr, o4.x, acc.x);
+              acc.y = fmaf(wr, o4.y, acc.y);
+              acc.z = fmaf(wr, o4.z, acc.z);
+              acc.w = fmaf(wr, o4.w, acc.w);
+            }
+            const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
+            const long long tok = (long long)w.s.c0 + w.i0 + itok;
+            const int head = w.h * p.G + g;
+            const long long oi = (tok * p.Hq + head) * D + c4;
+            if (dbg_range(ab, oi, 4, (long long)p.total * p.Hq * D))
+              *reinterpret_cast<uint2*>(p.o + oi) =
+                  make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            const long long li = (long long)head * p.total + tok;
+            if (c4 == 0 && dbg_range(ab, li, 1, (long long)p.Hq * p.total))
+              p.lse[li] = wsum == 0.0f ? -INFINITY : (m_sub + lg2_approx(wsum)) * kLn2;
+          }
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    if constexpr (kF8) {
+      // ---------------------------------------------------------------- E4M3 codes -> bf16 operand tiles
+      constexpr int kPerRow = D / 16;  // 16-byte pieces of codes in a row
+      const int ct = tid - 128 - Cfg::kSoftThreads;
+      const int c = ct % kPerRow;      // this thread's piece, in rows ct / kPerRow + k * (128 / kPerRow)
+      const int box_shift = 31 - __clz(p.box_rows);
+      uint32_t n = 0;
+      Walk w;
+      for (begin(w); w.valid(); w.next(p)) {
+        for (int v = w.v0; v < w.v1; ++v) {
+          const int key0 = w.keys.tile(v) * 128;
+  #pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const uint32_t rs = n % Cfg::kRawSlots, ks = n % Cfg::kSlots;
+            mbar_wait(bar(bars->raw_full[rs]), (n / Cfg::kRawSlots) & 1, ab);
+            mbar_wait(bar(bars->kv_empty[ks]), ((n / Cfg::kSlots) & 1) ^ 1, ab);
+            const uint8_t* raw = smem_gen + Cfg::kOffRaw + rs * Cfg::kRawSlotBytes;
+            const uint8_t* scale = raw + Cfg::kRawBytes;
+            const uint32_t dst = sKV + ks * Cfg::kTileBytes;
+  #pragma unroll 4
+            for (int k = 0; k < kPerRow; ++k) {
+              const int row = ct / kPerRow + k * (128 / kPerRow), key = key0 + row;
+              uint4 x = reinterpret_cast<const uint4*>(raw)[row * kPerRow + c];
+              uint32_t s = scale[((row >> box_shift) << 7) + (row & (p.box_rows - 1))];
+              // V rows that no row of the block sees may hold anything: 0 (their weights are 0)
+              if (kv && (key > w.keys.vis_hi || (key < w.keys.vis_lo && key >= p.sinks))) {
+                x = make_uint4(0u, 0u, 0u, 0u);
+                s = 127u;
+              }
+              const uint32_t f = (min(s, 134u) + 120u) << 7, ff = f | (f << 16);  // 2^(s - 127 + 120), bf16
+              const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+              uint32_t r[8];
+  #pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                r[2 * e] = mul_bf16x2(e4m3_pair_bits(__byte_perm(in[e], 0u, 0x1404)), ff);
+                r[2 * e + 1] = mul_bf16x2(e4m3_pair_bits(__byte_perm(in[e], 0u, 0x3424)), ff);
+              }
+              if (s > 134u) {  // scales above 2^7: a second factor; NaN for s = 255
+                const uint32_t g = s == (uint32_t)kScaleNan ? 0x7fc0u : (s - 134u + 127u) << 7;
+  #pragma unroll
+                for (int e = 0; e < 8; ++e) r[e] = mul_bf16x2(r[e], g | (g << 16));
+              }
+              // two 16-byte chunks; the upper half of a row's threads stores its odd chunk first,
+              // so that the eight threads of a row (d = 128) touch all banks in each store
+              const uint32_t b0 = dst + (uint32_t)(c >> 2) * 16384u;
+              const uint32_t a0 = b0 + sw128_offset(row, 2 * (c & 3)), a1 = b0 + sw128_offset(row, 2 * (c & 3) + 1);
+              if (c & 4) {
+                st_shared_v4(a1, r[4], r[5], r[6], r[7]);
+                st_shared_v4(a0, r[0], r[1], r[2], r[3]);
+              } else {
+                st_shared_v4(a0, r[0], r[1], r[2], r[3]);
+                st_shared_v4(a1, r[4], r[5], r[6], r[7]);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(bars->raw_empty[rs]));
+              mbar_arrive(bar(bars->kv_full[ks]));
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // the grid ends after the kernel that zeroes the counters, whether or not a CTA has joined a block
+  if (warp == 2) griddep_wait();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+}  // namespace fa

@@ -170,6 +170,80 @@ int fa_decode_paged(const void* q, void* k_cache, void* v_cache, const void* k_n
                     void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * Paged caches and ragged chunks (the pages' paged KV cache and in-place update, above, for any
+ * number of new rows and for quantised pages). The next three calls share these arguments:
+ *   cu_seqlens   device (B+1) int32: sequence b's new rows are the packed rows
+ *                [cu_seqlens[b], cu_seqlens[b+1]); cu_seqlens[0] = 0, non-decreasing,
+ *                cu_seqlens[B] <= total. Rows from cu_seqlens[B] on belong to no sequence:
+ *                they are not read, and the outputs' are left as they were.
+ *   seqlens      device (B) int32: keys of sequence b, its new rows included: row i of its new_b
+ *                rows sits at position seqlens[b] - new_b + i (a negative position has no place).
+ *   block_table  device (B,max_pages) int32, as fa_decode_paged; entries past a sequence's
+ *                length, or of pages that no row of a call can see, are not read.
+ *   k_cache,     bf16 pages (num_pages,page_size,H,d), with k_scale = v_scale = NULL; or E4M3
+ *   v_cache      codes (one byte each) of that shape with
+ *   k_scale,     (num_pages,H,page_size) scale bytes s, standing for 2^(s-127) (E8M0): element x
+ *   v_scale      of row (token, head) is decode(code) * 2^(s-127); s = 255 makes the row NaN. A
+ *                cache of scale bytes other than 17..255, or of NaN codes beside another scale, is
+ *                not one that fa_cache_write writes: such values are unspecified.
+ *                All four 16-byte aligned; page_size a multiple of 16 (FA_ERR_UNSUPPORTED).
+ * H (Hkv below) is the number of key/value heads, d is 64 or 128, max_pages * page_size and total
+ * are at most 2^30; total = 0 is a call without work. Lengths, offsets or page indices out of
+ * range are not followed: such a sequence or row counts as empty (as zeros where it is read) and
+ * fa_check() returns FA_ERR_DEVICE. Other errors as fa_fwd.
+ */
+
+/*
+ * Writes the new rows k_new, v_new (total,H,d) bf16, row_stride elements from a token's row to the
+ * next (a multiple of 8, >= H*d: slices of a fused projection are fine), into their pages. E4M3
+ * pages: for each (token, head), with a = max |x| over its d values and e the least integer
+ * >= -110 with a <= 448 * 2^e, the codes are E4M3(x * 2^-e), rounded to nearest even, and the
+ * scale byte is e + 127 (with e = 120 codes stop at 240, since 256 * 2^120 is beyond bf16); a row with a NaN or an infinity gets the scale byte 255. Two rows of one
+ * call must not have the same place. One launch on `stream`.
+ */
+int fa_cache_write(const void* k_new, const void* v_new, long long row_stride, void* k_cache, void* v_cache,
+                   void* k_scale, void* v_scale, const int* block_table, const int* seqlens, const int* cu_seqlens,
+                   int B, int total, int H, int d, int num_pages, int page_size, int max_pages, fa_stream_t stream);
+
+/*
+ * Reads the same rows back into k, v (total,H,d) bf16, row_stride elements apart as above: exactly
+ * (a code times its scale is a bf16 value; beyond bf16's range, which fa_cache_write does not
+ * write, an infinity). Rows without a place are zeros. One launch.
+ */
+int fa_cache_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                  const int* block_table, const int* seqlens, const int* cu_seqlens, void* k, void* v,
+                  long long row_stride, int B, int total, int H, int d, int num_pages, int page_size, int max_pages,
+                  fa_stream_t stream);
+
+/*
+ * Bytes of device workspace fa_chunk_paged needs on the current device (partial results of blocks
+ * that are spread over several CTAs, and their counters); 0 for invalid sizes.
+ */
+size_t fa_chunk_workspace_bytes(int B, int total, int Hq, int Hkv, int d);
+
+/*
+ * Attention of the new rows over the cache that already holds their keys and values: any number of
+ * rows per sequence, from one (a decoding step) to a whole prompt, in one batch.
+ *   q        (total,Hq,d) bf16, rows q_stride elements apart (a multiple of 8, >= Hq*d); query head h
+ *            reads key/value head h / (Hq/Hkv), Hq a multiple of Hkv (a quotient above 128:
+ *            FA_ERR_UNSUPPORTED).
+ *   o, lse   (total,Hq,d) bf16 and (Hq,total) float32 natural-log LSE; a row that sees no key gets
+ *            O = 0 and LSE = -inf.
+ * The row at position p of a sequence of n keys sees key j < n when j <= p + win_r (win_r = 0 when
+ * causal; -1: no bound), and j >= p - win_l (-1: no bound) or j < sinks: the sequence's first
+ * `sinks` keys stay visible left of the window. Masked scores carry no weight whatever K holds
+ * there; V rows that some row of the same 128- or 256-row block sees must be finite. Workspace of
+ * fa_chunk_workspace_bytes (256-byte aligned, any contents), or NULL to allocate on `stream`; calls
+ * that may overlap need workspaces of their own. Results do not depend on the order in which
+ * CTAs run. Two launches on `stream`.
+ */
+int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const void* k_scale,
+                   const void* v_scale, const int* block_table, const int* seqlens, const int* cu_seqlens, void* o,
+                   float* lse, int B, int total, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                   float scale, int causal, int win_l, int win_r, int sinks, void* workspace, size_t workspace_bytes,
+                   fa_stream_t stream);
+
+/*
  * Bytes of device workspace fa_bwd needs: a float32 dQ accumulator (B,N,H,d), two
  * float32 (B,H,ceil(N/128)*128) row vectors (-LSE*log2(e) and -D, D = rowsum(dO*O)) and a
  * 256-byte block holding the work counter of the main kernel, each region 256-byte

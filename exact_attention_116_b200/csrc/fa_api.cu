@@ -671,27 +671,36 @@ int make_map_scales(CUtensorMap* m, const void* base, int num_pages, int page_si
 int chunk_tiles(int B, int total, int G) { return (double)total * G <= 128.0 * B ? 1 : 2; }
 
 struct ChunkWorkspace {
-  size_t o_bytes, lse_bytes, count_bytes;
-  size_t bytes() const { return o_bytes + lse_bytes + count_bytes; }
+  size_t o_bytes, lse_bytes, split_bytes;
+  size_t bytes() const { return o_bytes + lse_bytes + split_bytes; }
 };
 ChunkWorkspace chunk_workspace(int pieces, int tiles, int d) {
   const size_t rows = (size_t)2 * pieces * tiles * 128;  // two partial slots per piece
-  return {align256(rows * d * 4), align256(rows * 4), align256((size_t)pieces * 4)};
+  return {align256(rows * d * 4), align256(rows * 4), align256((size_t)pieces * 16)};
 }
 
 template <int D, bool kF8, int kTiles>
 int chunk_launch(int grid, const CUtensorMap* m, const fa::ChunkParams& p, cudaStream_t stream) {
+  using Cfg = fa::ChunkCfg<D, kF8, kTiles>;
+  fa::fa_chunk_kernel<D, kF8, kTiles><<<grid, Cfg::kThreads, Cfg::kSmemBytes, stream>>>(m[0], m[1], m[2], m[3], m[4], p);
+  return launch_status();
+}
+
+// The join of blocks that are spread over several pieces, as the main kernel's programmatic dependent.
+template <int D>
+int chunk_merge_launch(int pieces, int tiles, const fa::ChunkParams& p, cudaStream_t stream) {
+  const int per_cta = fa::kMergeThreads / (D / 4);  // rows
+  const long long rows = std::min<long long>((long long)p.total * p.G, tiles * 128);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(fa::ChunkCfg<D, kF8, kTiles>::kThreads);
-  cfg.dynamicSmemBytes = fa::ChunkCfg<D, kF8, kTiles>::kSmemBytes;
+  cfg.gridDim = dim3(pieces, (unsigned)((rows + per_cta - 1) / per_cta));
+  cfg.blockDim = dim3(fa::kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fa::fa_chunk_kernel<D, kF8, kTiles>, m[0], m[1], m[2], m[3], m[4], p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, fa::fa_chunk_merge_kernel<D>, p, tiles * 128) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
@@ -1078,7 +1087,8 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   }
   // pieces: one per SM, and no more than the key tiles there can be
   const double blocks = (double)(total / (tiles * tq)) + std::min(B, total);
-  const double most = blocks * Hkv * ((max_keys + 127) / 128 + 1);
+  const int key_tiles = (max_keys + 127) / 128;
+  const double most = blocks * Hkv * key_tiles;
   const int pieces = most < sms ? (int)most : sms;
   int box_rows = 16;
   while (box_rows < 128 && page_size % (2 * box_rows) == 0) box_rows *= 2;
@@ -1121,13 +1131,14 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   p.lse = lse;
   p.o_part = static_cast<float*>(ws);
   p.lse_part = reinterpret_cast<float*>(static_cast<char*>(ws) + wb.o_bytes);
-  p.arrivals = reinterpret_cast<int*>(static_cast<char*>(ws) + wb.o_bytes + wb.lse_bytes);
+  p.split = reinterpret_cast<int4*>(static_cast<char*>(ws) + wb.o_bytes + wb.lse_bytes);
   if (log_enabled())
     std::fprintf(stderr, "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d pieces=%d box=%d win=(%d,%d) sinks=%d\n",
                  B, total, Hq, Hkv, d, f8, tiles, pieces, box_rows, win_l, win_r, sinks);
-  fa::fa_decode_prep_kernel<<<1, 256, 0, cs>>>(p.arrivals, pieces);
-  st = launch_status();
-  if (!st) st = d == 64 ? chunk_variant<64>(f8, tiles, pieces, m, p, cs) : chunk_variant<128>(f8, tiles, pieces, m, p, cs);
+  st = d == 64 ? chunk_variant<64>(f8, tiles, pieces, m, p, cs) : chunk_variant<128>(f8, tiles, pieces, m, p, cs);
+  // (with one key tile per block at most, or one piece, no block is spread over pieces)
+  if (!st && pieces > 1 && key_tiles > 1)
+    st = d == 64 ? chunk_merge_launch<64>(pieces, tiles, p, cs) : chunk_merge_launch<128>(pieces, tiles, p, cs);
   if (!workspace && cudaFreeAsync(ws, cs) != cudaSuccess && !st) st = FA_ERR_CUDA;
   return st;
 }

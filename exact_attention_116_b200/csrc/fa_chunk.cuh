@@ -17,8 +17,9 @@
 // the lists of all heads, one after another, are cut into P equal contiguous pieces, one per CTA
 // (one CTA per SM). So every CTA visits the same number of key tiles (within one), for decoding
 // steps, long prompts and mixtures alike. A block that lies in one piece is finished by its CTA;
-// otherwise each of its pieces writes a partial (O / l, log2 l + m) and the piece that arrives last
-// merges them by their log-sum-exp, in piece order (the same sum whichever arrives last).
+// otherwise each of its pieces writes a partial (O / l, log2 l + m) and fa_chunk_merge_kernel joins
+// them by their log-sum-exp. (The CTA that finished a block last used to join it: one CTA reading
+// all partials of 64 rows took 60 us of a 178 us call, 32 query heads over 131072 keys.)
 //
 // Both products run on the tensor core, with the forward's roles and order of issue: S_t(v + 1)
 // ahead of P V_t(v), a row's 128 scores split over two warps that exchange their maxima, P in
@@ -54,7 +55,8 @@ struct ChunkParams {
   float* lse;              // (Hq, total), natural log
   float* o_part;           // (2 P, kTiles * 128, d) fp32
   float* lse_part;         // (2 P, kTiles * 128), log2 domain
-  int* arrivals;           // (P) pieces of the block that starts in piece r and goes on, finished
+  int4* split;             // (P) the block that starts in piece r and goes on: first packed row, tokens
+                           // (0: none), head, 2 * last piece + (slot of piece r is 2 r + 1)
 };
 
 template <int D, bool kF8, int kTiles>
@@ -93,7 +95,6 @@ struct ChunkBars {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  int last_flag;            // merge: this piece arrived last
   int first_b, first_blk;   // the piece's first block
   long long first_start;    // its position on the head's list
   long long sums[32];       // scans
@@ -248,6 +249,43 @@ __device__ __forceinline__ void chunk_mask(float (&x)[kC], int kbase, int kmin, 
   }
 }
 
+// 2^x of a pair on the FMA pipe, as exp2_poly2 with a degree-5 polynomial (relative error 6e-8 of
+// the fit, 2e-7 with its float32 steps: that of ex2.approx): the log-sum-exp, an fp32 output, would
+// show the degree-3 polynomial's 7.5e-5 in rows of a few keys.
+constexpr float kExp2D0 = 1.000000051e+00f, kExp2D1 = 6.931467120e-01f, kExp2D2 = 2.402214209e-01f,
+                kExp2D3 = 5.551047092e-02f, kExp2D4 = 9.675267120e-03f, kExp2D5 = 1.318565354e-03f;
+__device__ __forceinline__ float2 exp2_poly5x2(float2 x_in) {
+  const float2 x = make_float2(fmaxf(x_in.x, -125.0f), fmaxf(x_in.y, -125.0f));
+  const float2 t = add2(x, make_float2(12582912.0f, 12582912.0f));
+  const float2 jf = add2(t, make_float2(-12582912.0f, -12582912.0f));
+  const float2 f = fma2(jf, make_float2(-1.0f, -1.0f), x);
+  float2 p = fma2(make_float2(kExp2D5, kExp2D5), f, make_float2(kExp2D4, kExp2D4));
+  p = fma2(p, f, make_float2(kExp2D3, kExp2D3));
+  p = fma2(p, f, make_float2(kExp2D2, kExp2D2));
+  p = fma2(p, f, make_float2(kExp2D1, kExp2D1));
+  p = fma2(p, f, make_float2(kExp2D0, kExp2D0));
+  const float rx = __int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23));
+  const float ry = __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23));
+  return make_float2(x_in.x >= -125.0f ? rx : 0.0f, x_in.y >= -125.0f ? ry : 0.0f);
+}
+
+// Exponentials of 32 scores (16 pairs from pair k0 on) against the reference maximum, packed to bf16
+// pairs and summed twice, as fwd_exp_chunk; one pair in eight takes the polynomial.
+template <bool kPosScale, int kC>
+__device__ __forceinline__ void chunk_exp(const float (&x)[kC], int k0, float c, float m_use, uint32_t (&pk)[16],
+                                          float2& sum, float2& rsum) {
+  const float2 neg_m = make_float2(-m_use, -m_use), c2 = make_float2(c, c);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 xv = make_float2(x[2 * (k0 + k)], x[2 * (k0 + k) + 1]);
+    const float2 a = kPosScale ? fma2(xv, c2, neg_m) : add2(xv, neg_m);
+    const float2 pv = k % 8 == 0 ? exp2_poly5x2(a) : make_float2(ex2_approx(a.x), ex2_approx(a.y));
+    sum = add2(sum, pv);
+    pk[k] = pack_bf16x2(pv.x, pv.y);
+    rsum = add_bf16x2_f32x2(pk[k], rsum);
+  }
+}
+
 template <int D, bool kF8, int kTiles>
 __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     fa_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -267,6 +305,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
   const Abort ab{&bars->abort_flag};
   const long long max_keys = (long long)p.max_pages * p.page_size;
 
+  griddep_launch_dependents();  // the merge takes an SM as soon as its CTA is done, and waits there
   if (tid == 0) {
     bars->abort_flag = 0;
     for (int t = 0; t < 2; ++t) {
@@ -553,6 +592,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     const bool pos_scale = c > 0.0f;
     const int tok_in_tile = row / p.G, head_in_group = row - tok_in_tile * p.G;
 
+    int4 split = make_int4(0, 0, 0, 0);  // the block that this piece hands on to the next one
     Walk w;
     for (begin(w); w.valid(); w.next(p)) {
       const int nv = w.v1 - w.v0;
@@ -629,9 +669,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         for (int q4 = 0; q4 < kC / 32; ++q4) {
           uint32_t pk[16];
           if (pos_scale)
-            fwd_exp_chunk<true>(x, q4 * 16, c, m_use, pk, sum, rsum);
+            chunk_exp<true>(x, q4 * 16, c, m_use, pk, sum, rsum);
           else
-            fwd_exp_chunk<false>(x, q4 * 16, c, m_use, pk, sum, rsum);
+            chunk_exp<false>(x, q4 * 16, c, m_use, pk, sum, rsum);
           tmem_st16(tP + q4 * 16, pk);
         }
         l_run = l_run * alpha + (sum.x + sum.y);
@@ -734,54 +774,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         tc_fence_before_sync();
       }
       vn += nv;
-
-      if (pf != pl) {
-        // ---- the block is spread over pieces pf..pl: the last one to arrive merges
-        __threadfence();  // this thread's partials are visible device-wide before the arrival
-        named_bar_sync(1, Cfg::kSoftThreads);
-        if (st == 0) {
-          griddep_wait();  // the arrival counters have been zeroed
-          const int before = dbg_range(ab, pf, 1, p.pieces) ? atomicAdd(&p.arrivals[pf], 1) : -1;
-          bars->last_flag = before == pl - pf;
-        }
-        named_bar_sync(1, Cfg::kSoftThreads);
-        if (bars->last_flag) {
-          __threadfence();
-          const int brows = w.ntok * p.G;  // rows of the block: tile 1's start at row 128 of a slot
-          for (int e = st; e < brows * (D / 4); e += Cfg::kSoftThreads) {
-            const int rr = e / (D / 4), c4 = (e - rr * (D / 4)) * 4;
-            const int itok = rr / p.G, g = rr - itok * p.G, tile = itok >= p.tq ? 1 : 0;
-            const int srow = tile * 128 + rr - tile * p.tq * p.G;
-            auto prow_of = [&](int r) { return (long long)slot_of(r) * (kTiles * 128) + srow; };
-            float mx = -INFINITY;
-            for (int r = pf; r <= pl; ++r) mx = fmaxf(mx, __ldcg(p.lse_part + prow_of(r)));
-            float wsum = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const float m_sub = mx == -INFINITY ? 0.0f : mx;
-            for (int r = pf; r <= pl; ++r) {
-              const long long pr = prow_of(r);
-              const float wr = ex2_approx(__ldcg(p.lse_part + pr) - m_sub);
-              const float4 o4 = __ldcg(reinterpret_cast<const float4*>(p.o_part + pr * D + c4));
-              wsum += wr;
-              acc.x = fmaf(wr, o4.x, acc.x);
-              acc.y = fmaf(wr, o4.y, acc.y);
-              acc.z = fmaf(wr, o4.z, acc.z);
-              acc.w = fmaf(wr, o4.w, acc.w);
-            }
-            const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
-            const long long tok = (long long)w.s.c0 + w.i0 + itok;
-            const int head = w.h * p.G + g;
-            const long long oi = (tok * p.Hq + head) * D + c4;
-            if (dbg_range(ab, oi, 4, (long long)p.total * p.Hq * D))
-              *reinterpret_cast<uint2*>(p.o + oi) =
-                  make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-            const long long li = (long long)head * p.total + tok;
-            if (c4 == 0 && dbg_range(ab, li, 1, (long long)p.Hq * p.total))
-              p.lse[li] = wsum == 0.0f ? -INFINITY : (m_sub + lg2_approx(wsum)) * kLn2;
-          }
-        }
-      }
+      if (pf != pl && pf == piece)
+        split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * pl + (dec_piece_lo(T, pe, pf) < w.start ? 1 : 0));
     }
+    if (st == 0 && dbg_range(ab, blockIdx.x, 1, p.pieces)) p.split[blockIdx.x] = split;
   } else if (warp >= 4) {
     if constexpr (kF8) {
       // ---------------------------------------------------------------- E4M3 codes -> bf16 operand tiles
@@ -849,12 +845,64 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     }
   }
 
-  // the grid ends after the kernel that zeroes the counters, whether or not a CTA has joined a block
-  if (warp == 2) griddep_wait();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+// Joins the blocks that are spread over several pieces: CTA (r, y) takes the block that starts in
+// piece r and goes on, if there is one, and of it the rows y, y + gridDim.y, ... (in groups). A row's
+// partials are weighted by 2^(their log-sum-exp - the largest), in piece order: the same sum in
+// every run. d / 4 threads per row, 16 bytes each; bound by the latency of the partials, which lie
+// in L2, so eight of them are in flight per thread. Launched as the main kernel's programmatic
+// dependent: it is resident by the time the last piece is written.
+constexpr int kMergeThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const ChunkParams p, int tile_rows) {
+  constexpr int kLanes = D / 4, kRows = kMergeThreads / kLanes;
+  const Abort none{nullptr};
+  griddep_wait();  // the pieces have been written
+  const int pf = blockIdx.x;
+  const int4 s = __ldcg(p.split + pf);
+  const int rows = s.y * p.G, pl = s.w >> 1;
+  const int c4 = (threadIdx.x % kLanes) * 4;
+  const long long part_rows = 2LL * p.pieces * tile_rows;
+  for (int first = blockIdx.y * kRows; first < rows; first += gridDim.y * kRows) {
+    const int rr = first + threadIdx.x / kLanes;
+    if (rr >= rows) break;
+    const int itok = rr / p.G, g = rr - itok * p.G, tile = itok >= p.tq ? 1 : 0;
+    const int srow = tile * 128 + rr - tile * p.tq * p.G;
+    auto prow_of = [&](int r) { return (2LL * r + (r == pf ? (s.w & 1) : 0)) * tile_rows + srow; };
+    if (!dbg_range(none, prow_of(pf), 1, part_rows) || !dbg_range(none, prow_of(pl), 1, part_rows)) break;
+    float mx = -INFINITY;
+#pragma unroll 8
+    for (int r = pf; r <= pl; ++r) mx = fmaxf(mx, __ldcg(p.lse_part + prow_of(r)));
+    float wsum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float m_sub = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll 8
+    for (int r = pf; r <= pl; ++r) {
+      const long long pr = prow_of(r);
+      const float wr = ex2_approx(__ldcg(p.lse_part + pr) - m_sub);
+      const float4 o4 = __ldcg(reinterpret_cast<const float4*>(p.o_part + pr * D + c4));
+      wsum += wr;
+      acc.x = fmaf(wr, o4.x, acc.x);
+      acc.y = fmaf(wr, o4.y, acc.y);
+      acc.z = fmaf(wr, o4.z, acc.z);
+      acc.w = fmaf(wr, o4.w, acc.w);
+    }
+    const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
+    const long long tok = (long long)s.x + itok;
+    const int head = s.z * p.G + g;
+    const long long oi = (tok * p.Hq + head) * D + c4;
+    if (dbg_range(none, oi, 4, (long long)p.total * p.Hq * D))
+      *reinterpret_cast<uint2*>(p.o + oi) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    const long long li = (long long)head * p.total + tok;
+    if (c4 == 0 && dbg_range(none, li, 1, (long long)p.Hq * p.total))
+      p.lse[li] = wsum == 0.0f ? -INFINITY : (m_sub + lg2_approx(wsum)) * kLn2;
   }
 }
 

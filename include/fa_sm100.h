@@ -217,7 +217,7 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const void* k_scale,
 
 /*
  * Bytes of device workspace fa_chunk_paged needs on the current device (partial results of blocks
- * that are spread over several CTAs, and their counters); 0 for invalid sizes.
+ * that are spread over several CTAs); 0 for invalid sizes.
  */
 size_t fa_chunk_workspace_bytes(int B, int total, int Hq, int Hkv, int d);
 
@@ -235,7 +235,7 @@ size_t fa_chunk_workspace_bytes(int B, int total, int Hq, int Hkv, int d);
  * there; V rows that some row of the same 128- or 256-row block sees must be finite. Workspace of
  * fa_chunk_workspace_bytes (256-byte aligned, any contents), or NULL to allocate on `stream`; calls
  * that may overlap need workspaces of their own. Results do not depend on the order in which
- * CTAs run. Two launches on `stream`.
+ * CTAs run. One or two launches on `stream`.
  */
 int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const void* k_scale,
                    const void* v_scale, const int* block_table, const int* seqlens, const int* cu_seqlens, void* o,

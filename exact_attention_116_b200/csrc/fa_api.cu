@@ -670,6 +670,12 @@ int make_map_scales(CUtensorMap* m, const void* base, int num_pages, int page_si
 // chunks need; with at most one tile of rows per sequence on average the second would stand idle.
 int chunk_tiles(int B, int total, int G) { return (double)total * G <= 128.0 * B ? 1 : 2; }
 
+fa::FastDiv fast_div(unsigned d) {
+  unsigned s = 0;
+  while ((1ull << s) < d) ++s;
+  return {(unsigned)((((1ull << 32) << s) + d - 1) / d - (1ull << 32)), s};
+}
+
 struct ChunkWorkspace {
   size_t o_bytes, lse_bytes, split_bytes;
   size_t bytes() const { return o_bytes + lse_bytes + split_bytes; }
@@ -689,10 +695,9 @@ int chunk_launch(int grid, const CUtensorMap* m, const fa::ChunkParams& p, cudaS
 // The join of blocks that are spread over several pieces, as the main kernel's programmatic dependent.
 template <int D>
 int chunk_merge_launch(int pieces, int tiles, const fa::ChunkParams& p, cudaStream_t stream) {
-  const int per_cta = fa::kMergeThreads / (D / 4);  // rows
   const long long rows = std::min<long long>((long long)p.total * p.G, tiles * 128);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pieces, (unsigned)((rows + per_cta - 1) / per_cta));
+  cfg.gridDim = dim3(pieces, (unsigned)((rows + fa::kMergeRows - 1) / fa::kMergeRows));
   cfg.blockDim = dim3(fa::kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -700,7 +705,7 @@ int chunk_merge_launch(int pieces, int tiles, const fa::ChunkParams& p, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fa::fa_chunk_merge_kernel<D>, p, tiles * 128) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, fa::fa_chunk_merge_kernel<D>, p, tiles) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
@@ -1116,6 +1121,9 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   p.G = G;
   p.tq = tq;
   p.page_size = page_size;
+  p.by_page = fast_div(page_size);
+  p.by_group = fast_div(G);
+  p.by_tokens = fast_div(tiles * tq);
   p.box_rows = box_rows;
   p.max_pages = max_pages;
   p.num_pages = num_pages;

@@ -48,11 +48,11 @@ struct CacheParams {
 
 // Offsets and lengths of a ragged batch over a paged cache: reports (kErrBadInput) offsets that
 // do not start at 0, decrease or pass `total`, and lengths outside [0, max_pages * page_size].
-// Called by all threads of one block.
+// Called by `threads` threads of one block, `tid` of them.
 __device__ __forceinline__ void report_bad_batch(const int* cu, const int* seqlens, int B, int total,
-                                                 long long max_keys) {
-  bool bad = threadIdx.x == 0 && (cu[0] != 0 || cu[B] > total);
-  for (int i = threadIdx.x; i < B; i += blockDim.x)
+                                                 long long max_keys, int tid, int threads) {
+  bool bad = tid == 0 && (cu[0] != 0 || cu[B] > total);
+  for (int i = tid; i < B; i += threads)
     bad |= cu[i + 1] < cu[i] || seqlens[i] < 0 || seqlens[i] > max_keys;
   if (bad) atomicOr(&g_fa_error, kErrBadInput);
 }
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_write_kernel(const Cac
   constexpr int kLanes = D / 8;                  // lanes of one row
   const Abort none{nullptr};
   if (blockIdx.x == 0)
-    report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size);
+    report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, threadIdx.x, kCacheThreads);
   const long long unit = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
   const int lane = lane_id();
   const int token = (int)(unit / p.parts), part = (int)(unit - (long long)token * p.parts);
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const Cach
   constexpr int kIters = kCacheWarpElems / (32 * kVec);
   const Abort none{nullptr};
   if (blockIdx.x == 0)
-    report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size);
+    report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, threadIdx.x, kCacheThreads);
   const long long unit = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
   const int lane = lane_id();
   const int token = (int)(unit / p.parts), part = (int)(unit - (long long)token * p.parts);

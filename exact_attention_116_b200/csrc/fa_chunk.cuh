@@ -38,10 +38,18 @@
 
 namespace fa {
 
+// Division of 0 <= n < 2^31 by a number known on the host: n / d = (n + hi(n m)) >> s with
+// s = ceil(log2 d), m = ceil(2^(32 + s) / d) - 2^32.
+struct FastDiv {
+  unsigned m, s;
+  __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi((unsigned)n, m) + (unsigned)n) >> s); }
+};
+
 struct ChunkParams {
   int B, total, Hq, Hkv, G;
   int tq;          // tokens per 128-row tile: 128 / G
   int page_size;
+  FastDiv by_page, by_group, by_tokens;  // page_size, G, tokens of a block (kTiles * tq)
   int box_rows;    // rows of one page box: the largest power of two that divides page_size, <= 128
   int max_pages, num_pages;
   float scale_log2;  // scale * log2(e)
@@ -53,24 +61,33 @@ struct ChunkParams {
   const int* cu;           // (B + 1)
   __nv_bfloat16* o;        // (total, Hq, d)
   float* lse;              // (Hq, total), natural log
-  float* o_part;           // (2 P, kTiles * 128, d) fp32
+  float* o_part;           // (2 P, kTiles, d / 4, 128, 4) fp32: a warp's rows lie side by side
   float* lse_part;         // (2 P, kTiles * 128), log2 domain
   int4* split;             // (P) the block that starts in piece r and goes on: first packed row, tokens
                            // (0: none), head, 2 * last piece + (slot of piece r is 2 r + 1)
 };
 
+#ifndef FA_S
+#define FA_S (kTiles == 2 ? 2 : 2)
+#define FA_R (kTiles == 2 ? 5 : 7)
+#endif
 template <int D, bool kF8, int kTiles>
 struct ChunkCfg {
   static constexpr int kSoftWarps = 8 * kTiles;       // row split: two warps per 32 rows
   static constexpr int kSoftThreads = 32 * kSoftWarps;
-  static constexpr int kConvThreads = kF8 ? 128 : 0;
+  static constexpr int kConvThreads = kF8 ? 256 : 0;
+  static constexpr int kConvWarps = kConvThreads / 32;
   static constexpr int kThreads = 128 + kSoftThreads + kConvThreads;
+  static constexpr int kRegs = 65536 / kThreads / 8 * 8;  // a thread's at launch
+  static constexpr int kLoadRegs = 56, kConvRegs = kTiles == 2 ? 48 : 64;
+  static constexpr int kSoftRegs = kTiles == 2 ? (kF8 ? 88 : 104) : kF8 ? 128 : 0;  // 0: as launched
+  static_assert(kSoftRegs * kSoftThreads + kLoadRegs * 128 + kConvRegs * kConvThreads <= kRegs * kThreads, "registers");
   static constexpr int kBoxes = D / 64;               // 128-byte boxes per bf16 row
   static constexpr int kTileBytes = 128 * D * 2;      // a bf16 tile of Q, K or V
   static constexpr int kRawBytes = 128 * D;           // the codes of a K or V tile
   static constexpr int kRawSlotBytes = kRawBytes + 1024;  // codes, then the scales of each page box at 128 bytes
-  static constexpr int kSlots = kF8 ? (D == 64 ? 6 : kTiles == 2 ? 3 : 4) : (D == 64 ? 10 : kTiles == 2 ? 4 : 5);
-  static constexpr int kRawSlots = kF8 ? (D == 64 ? 6 : 3) : 0;
+  static constexpr int kSlots = kF8 ? (D == 64 ? 4 : FA_S) : (D == 64 ? 10 : kTiles == 2 ? 4 : 5);
+  static constexpr int kRawSlots = kF8 ? (D == 64 ? (kTiles == 2 ? 12 : 14) : FA_R) : 0;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = kTiles * kTileBytes;
   static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
@@ -95,9 +112,10 @@ struct ChunkBars {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  int first_b, first_blk;   // the piece's first block
-  long long first_start;    // its position on the head's list
-  long long sums[32];       // scans
+  long long u0, u1, th;     // the piece, the length of one head's list
+  long long first_start;    // the piece's first block: its position on the list of all heads
+  int first_h, first_b, first_blk;
+  long long sums[2][4];     // scans
 };
 
 // A sequence: first packed row, rows and keys. Offsets or lengths out of range make it empty
@@ -140,10 +158,11 @@ __device__ __forceinline__ ChunkKeys chunk_keys(const ChunkParams& p, int n, int
 }
 
 // A walk over the blocks of one piece. A block: head h, sequence b, tokens [i0, i0 + ntok) of its
-// chunk; its tiles [v0, v1) belong to the piece.
+// chunk; its tiles [v0, v1) belong to the piece. It lies in the piece as a whole (whole()), or is
+// spread over several.
 template <int kTiles>
 struct ChunkWalk {
-  long long u0, u1, th;  // the piece's range of the list of all heads, the length of one head's list
+  long long u0, u1;  // the piece's range of the list of all heads
   int h, b, blk;
   ChunkSeq s;
   ChunkKeys keys;
@@ -160,16 +179,16 @@ struct ChunkWalk {
     v1 = (int)min((long long)keys.cnt, u1 - start);
   }
   __device__ __forceinline__ bool valid() const { return start < u1; }
-  __device__ __forceinline__ void begin(const ChunkParams& p, int h_, int b_, int blk_, long long start_, long long u0_,
-                                        long long u1_, long long th_) {
-    u0 = u0_;
-    u1 = u1_;
-    th = th_;
-    h = h_;
-    b = b_;
-    blk = blk_;
-    start = start_;
+  __device__ __forceinline__ bool whole() const { return start >= u0 && start + keys.cnt <= u1; }
+  template <class Bars>
+  __device__ __forceinline__ void begin(const ChunkParams& p, const Bars* bars) {
+    u0 = bars->u0;
+    u1 = bars->u1;
+    start = bars->first_start;
     if (!valid()) return;
+    h = bars->first_h;
+    b = bars->first_b;
+    blk = bars->first_blk;
     s = chunk_seq(p, b);
     set(p);
   }
@@ -191,24 +210,126 @@ struct ChunkWalk {
   __device__ __forceinline__ int pos0(int tq, int t) const { return s.n - s.rows + i0 + t * tq; }
 };
 
-// Inclusive scan over the block's threads of non-negative counts; scratch holds 32 values.
-__device__ __forceinline__ long long block_scan(long long x, long long* scratch, long long& total) {
-  const int warp = threadIdx.x >> 5, lane = lane_id(), warps = blockDim.x >> 5;
+// The list of all heads, T tiles, in pieces: the first T % pieces of them one tile longer.
+struct ChunkSplit {
+  long long each, more;
+  __device__ __forceinline__ ChunkSplit(long long T, int pieces) {
+    if (T < (1LL << 31)) {  // (a 64-bit division is some 100 instructions)
+      each = (unsigned)T / (unsigned)pieces;
+    } else {
+      each = T / pieces;
+    }
+    more = T - each * pieces;
+  }
+  __device__ __forceinline__ long long lo(int r) const { return each * r + min((long long)r, more); }
+  __device__ __forceinline__ int of(long long u) const {  // the piece that holds tile u
+    const long long head = more * (each + 1);
+    return u < head ? (int)(u / (each + 1)) : (int)(more + (u - head) / each);
+  }
+};
+
+// Pieces of a list of T tiles: with less than kMinPiece tiles each, CTAs would spend more time on
+// setting up and joining than on tiles.
+constexpr int kMinPiece = 2;
+__device__ __forceinline__ int chunk_pieces(const ChunkParams& p, long long T) {
+  return (int)min((long long)p.pieces, max(1LL, T / kMinPiece));
+}
+
+// The set-up of one CTA by 128 threads (tid 0..127 here): which piece is its own, and where the
+// piece's first block lies. Blocks are counted per run of sequences, then key tiles per run of
+// blocks. (All the CTA's warps used to take part: what bounds this is the issue of its
+// instructions, several thousand cycles with 20 warps.)
+constexpr int kPlanThreads = 128;
+__device__ __forceinline__ long long plan_scan(long long x, long long (&sums)[4], int tid, long long& total) {
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const long long v = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += v;
+    if ((tid & 31) >= off) x += v;
   }
-  __syncthreads();  // the scratch of an earlier scan has been read
-  if (lane == 31) scratch[warp] = x;
-  __syncthreads();
-  total = 0;
-  long long before = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
+  if ((tid & 31) == 31) sums[tid >> 5] = x;
+  named_bar_sync(1, kPlanThreads);
+  const long long a = sums[0], b = a + sums[1], c = b + sums[2];
+  total = c + sums[3];
+  const int w = tid >> 5;
+  return x + (w == 0 ? 0 : w == 1 ? a : w == 2 ? b : c);
+}
+template <int kTiles, class Bars>
+__device__ __forceinline__ void chunk_plan(const ChunkParams& p, Bars* bars, int* run_base, int tid) {
+  const int run = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int rb0 = min(p.B, tid * run), rb1 = min(p.B, rb0 + run);
+  const int tokens = kTiles * p.tq;
+  auto blocks_of = [&](const ChunkSeq& s) { return p.by_tokens(s.rows + tokens - 1); };
+  long long blocks = 0, nb;
+  for (int b = rb0; b < rb1; ++b) blocks += blocks_of(chunk_seq(p, b));
+  const long long blocks_incl = plan_scan(blocks, bars->sums[0], tid, nb);
+  run_base[tid] = (int)(blocks_incl - blocks);
+  named_bar_sync(1, kPlanThreads);
+  // this thread's blocks [q0, q1): found by the run of sequences that holds q0
+  const long long each = (nb + kPlanThreads - 1) / kPlanThreads;
+  const long long q0 = min(nb, each * tid), q1 = min(nb, q0 + each);
+  int b = 0, blk = 0;
+  if (q0 < q1) {
+    int lo = 0;
+#pragma unroll
+    for (int step = kPlanThreads / 2; step > 0; step >>= 1)
+      if (run_base[lo + step] <= q0) lo += step;
+    b = lo * run;
+    blk = (int)(q0 - run_base[lo]);
   }
-  return x + before;
+  // visit the thread's blocks in order; f(b, blk, tiles of the block) until it returns false
+  auto visit = [&](auto f) {
+    int bb = b, kk = blk;
+    for (long long q = q0; q < q1;) {
+      const ChunkSeq s = chunk_seq(p, bb);
+      const int nbb = blocks_of(s);
+      if (kk >= nbb) {
+        kk -= nbb;
+        ++bb;
+        continue;
+      }
+      const int i0 = kk * tokens, pos0 = s.n - s.rows + i0;
+      if (!f(bb, kk, chunk_keys(p, s.n, pos0, pos0 + min(tokens, s.rows - i0) - 1).cnt)) return;
+      ++kk;
+      ++q;
+    }
+  };
+  long long tiles = 0, th;
+  visit([&](int, int, int cnt) {
+    tiles += cnt;
+    return true;
+  });
+  const long long tiles_incl = plan_scan(tiles, bars->sums[1], tid, th), excl = tiles_incl - tiles;
+  const long long T = th * p.Hkv;
+  const int pe = chunk_pieces(p, T), r = blockIdx.x;
+  long long u0 = T, u1 = T;
+  if (r < pe && T > 0) {
+    const ChunkSplit split(T, pe);
+    u0 = split.lo(r);
+    u1 = split.lo(r + 1);
+  }
+  if (tid == 0) {
+    bars->u0 = u0;
+    bars->u1 = u1;
+    bars->th = th;
+    if (u0 >= u1) bars->first_start = u1;
+  }
+  if (u0 >= u1) return;
+  const int h = u0 < (1LL << 31) && th < (1LL << 31) ? (int)((unsigned)u0 / (unsigned)th) : (int)(u0 / th);
+  const long long w0 = u0 - (long long)h * th;
+  if (excl <= w0 && w0 < tiles_incl) {
+    long long at = excl;
+    visit([&](int bb, int kk, int cnt) {
+      if (w0 >= at + cnt) {
+        at += cnt;
+        return true;
+      }
+      bars->first_h = h;
+      bars->first_b = bb;
+      bars->first_blk = kk;
+      bars->first_start = at + (long long)h * th;
+      return false;
+    });
+  }
 }
 
 // E4M3 codes, four in a word, to bf16 values times f (two packed factors per row: f, and g for
@@ -306,120 +427,49 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
   const long long max_keys = (long long)p.max_pages * p.page_size;
 
   griddep_launch_dependents();  // the merge takes an SM as soon as its CTA is done, and waits there
-  if (tid == 0) {
-    bars->abort_flag = 0;
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(bars->q_full[t]), 1);
-      mbar_init(bar(bars->q_empty[t]), 1);
-      mbar_init(bar(bars->s_full[t]), 1);
-      mbar_init(bar(bars->s_empty[t]), 256);
-      mbar_init(bar(bars->p_full[t]), 256);
-      mbar_init(bar(bars->pv_done[t]), 1);
+  // set-up, a part per warp: barriers (a lane each), TMEM, tensor maps, and the piece of this CTA
+  if (warp == 2) {
+    if (lane == 0) bars->abort_flag = 0;
+    constexpr int kBars = offsetof(Bars, mma_done) / 8 + 1, kPer = (kBars + 31) / 32;
+    constexpr int kKv = offsetof(Bars, kv_full) / 8, kRaw = offsetof(Bars, raw_full) / 8, kS = offsetof(Bars, s_full) / 8;
+    const uint32_t first = bar(bars->q_full[0]);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = lane + 32 * j;
+      int count = 1;
+      if (kF8 && i >= kKv && i < kKv + Cfg::kSlots) count = Cfg::kConvWarps;               // kv_full: converting warps
+      if (kF8 && i >= kRaw + Cfg::kRawSlots + 1 && i < kS) count = Cfg::kConvWarps;         // raw_empty
+      if (i >= kS + 2 && i < kS + 6) count = 256;                                           // s_empty, p_full
+      if (i < kBars) mbar_init(first + i * 8, count);
     }
-    for (int s = 0; s < Cfg::kSlots; ++s) {
-      mbar_init(bar(bars->kv_full[s]), kF8 ? 4 : 1);  // one arrival per converting warp, or the loads'
-      mbar_init(bar(bars->kv_empty[s]), 1);
-    }
-    for (int s = 0; s < Cfg::kRawSlots; ++s) {
-      mbar_init(bar(bars->raw_full[s]), 1);
-      mbar_init(bar(bars->raw_empty[s]), 4);
-    }
-    mbar_init(bar(bars->mma_done), 1);
     fence_barrier_init();
-    prefetch_tmap(&tmQ);
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-  }
-  if (warp == 1) {
+  } else if (warp == 1) {
     tmem_alloc(smem_u32(&bars->tmem_base), Cfg::kTmemCols);
     tmem_relinquish();
     tc_fence_before_sync();
-  }
-
-  // ---- the piece of this CTA: blocks per run of sequences, then key tiles per run of blocks
-  long long u0, u1, th;
-  {
-    if (blockIdx.x == 0) report_bad_batch(p.cu, p.seqlens, p.B, p.total, max_keys);
-    const int nthr = Cfg::kThreads, tokens = kTiles * p.tq;
-    int* run_base = reinterpret_cast<int*>(smem_gen);  // [kThreads], over the Q buffer (no load is in flight yet)
-    const int run = (p.B + nthr - 1) / nthr;
-    const int rb0 = min(p.B, tid * run), rb1 = min(p.B, rb0 + run);
-    long long blocks = 0;
-    for (int b = rb0; b < rb1; ++b) blocks += (chunk_seq(p, b).rows + tokens - 1) / tokens;
-    long long nb;
-    const long long blocks_incl = block_scan(blocks, bars->sums, nb);
-    run_base[tid] = (int)(blocks_incl - blocks);
-    __syncthreads();
-    // this thread's blocks [q0, q1): found by the run of sequences that holds q0
-    const long long q0 = nb * tid / nthr, q1 = nb * (tid + 1) / nthr;
-    int b = 0, blk = 0;
-    long long tiles = 0;
-    if (q0 < q1) {
-      int lo = 0, hi = nthr - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (run_base[mid] <= q0) lo = mid;
-        else hi = mid - 1;
-      }
-      b = lo * run;
-      blk = (int)(q0 - run_base[lo]);
+  } else if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
     }
-    // visit the thread's blocks in order; f(b, blk, tiles of the block) until it returns false
-    auto visit = [&](auto f) {
-      int bb = b, kk = blk;
-      for (long long q = q0; q < q1;) {
-        const ChunkSeq s = chunk_seq(p, bb);
-        const int nbb = (s.rows + tokens - 1) / tokens;
-        if (kk >= nbb) {
-          kk -= nbb;
-          ++bb;
-          continue;
-        }
-        const int i0 = kk * tokens, pos0 = s.n - s.rows + i0;
-        if (!f(bb, kk, chunk_keys(p, s.n, pos0, pos0 + min(tokens, s.rows - i0) - 1).cnt)) return;
-        ++kk;
-        ++q;
-      }
-    };
-    visit([&](int, int, int cnt) {
-      tiles += cnt;
-      return true;
-    });
-    const long long tiles_incl = block_scan(tiles, bars->sums, th);
-    const long long T = th * p.Hkv;
-    const int pe = (int)min((long long)p.pieces, T);
-    const int r = blockIdx.x;
-    u0 = r < pe ? dec_piece_lo(T, pe, r) : T;
-    u1 = r < pe ? dec_piece_lo(T, pe, r + 1) : T;
-    const long long w0 = th > 0 ? u0 % th : 0, excl = tiles_incl - tiles;
-    if (u0 < u1 && excl <= w0 && w0 < tiles_incl) {
-      long long at = excl;
-      visit([&](int bb, int kk, int cnt) {
-        if (w0 >= at + cnt) {
-          at += cnt;
-          return true;
-        }
-        bars->first_b = bb;
-        bars->first_blk = kk;
-        bars->first_start = at;
-        return false;
-      });
-    }
-    fence_proxy_async_smem();  // run_base has been read: the Q loads may overwrite it
+  } else if (warp >= 4 && warp < 8) {
+    // (over the Q buffer: no load is in flight yet)
+    chunk_plan<kTiles>(p, bars, reinterpret_cast<int*>(smem_gen), tid - 128);
+    fence_proxy_async_smem();  // the Q loads may overwrite it
   }
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
   const uint32_t sKV = smem_base + Cfg::kOffKV, sRaw = smem_base + Cfg::kOffRaw;
   auto sQ = [&](int t) { return smem_base + Cfg::kOffQ + t * Cfg::kTileBytes; };
-  const int h0 = th > 0 ? (int)(u0 / th) : 0;
-  auto begin = [&](Walk& w) {
-    if (u0 < u1)
-      w.begin(p, h0, bars->first_b, bars->first_blk, bars->first_start + (long long)h0 * th, u0, u1, th);
-    else
-      w.begin(p, 0, 0, 0, u1, u1, u1, th);
-  };
+  auto begin = [&](Walk& w) { w.begin(p, bars); };
 
+  // Registers: the launch gives each thread the same number (Cfg::kRegs); the producer and MMA warps
+  // and the converting ones hand some back, and the softmax warps take them. The sum stays within
+  // the launch's.
+  if (warp < 4) {
+  if constexpr (Cfg::kSoftRegs > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kLoadRegs) : "memory");
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (all lanes)
     // Lane l loads page box l % groups of 64-column box l / groups (E4M3: lanes from 16 on the
@@ -439,10 +489,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       page = p.num_pages;
       row = 0;
       if (!loads || key > x.keys.vis_hi || (last < x.keys.vis_lo && key >= p.sinks)) return;
-      const long long ti = (long long)x.b * p.max_pages + key / p.page_size;
+      const int in_seq = p.by_page(key);
+      const long long ti = (long long)x.b * p.max_pages + in_seq;
       if (!dbg_range(ab, ti, 1, (long long)p.B * p.max_pages)) return;
       page = __ldg(p.block_table + ti);
-      row = key % p.page_size;
+      row = key - in_seq * p.page_size;
       if (page < 0 || page >= p.num_pages) {
         atomicOr(&g_fa_error, kErrBadInput);
         page = p.num_pages;
@@ -510,6 +561,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     if (lane == 0)
       for (int t = 0; t < 2; ++t)
         if (qn[t] > 0) mbar_drain(bar(bars->q_full[t]), (qn[t] - 1) & 1);
+  } else if (warp == 3) {
+    if (blockIdx.x == 0) report_bad_batch(p.cu, p.seqlens, p.B, p.total, max_keys, lane, 32);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (elect_one()) {
@@ -573,7 +626,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       mma_commit(bar(bars->mma_done));
       mbar_drain(bar(bars->mma_done), 0);
     }
-  } else if (warp >= 4 && warp < 4 + Cfg::kSoftWarps) {
+  }
+  } else if (warp < 4 + Cfg::kSoftWarps) {
+    if constexpr (Cfg::kSoftRegs > 0)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kSoftRegs) : "memory");
     // ---------------------------------------------------------------- softmax + epilogue
     constexpr int kC = 64;                                    // scores of a row per thread and key tile
     const int t = kTiles == 2 ? ((warp - 4) >> 2) & 1 : 0;    // tile of the block
@@ -590,7 +646,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     auto pair_sync = [&]() { named_bar_sync(4 + 4 * t + (row >> 5), 64); };
     const float c = p.scale_log2;
     const bool pos_scale = c > 0.0f;
-    const int tok_in_tile = row / p.G, head_in_group = row - tok_in_tile * p.G;
+    const int tok_in_tile = p.by_group(row), head_in_group = row - tok_in_tile * p.G;
 
     int4 split = make_int4(0, 0, 0, 0);  // the block that this piece hands on to the next one
     Walk w;
@@ -696,13 +752,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
             const uint32_t vi = 2 * (vn + v) + 1, vs = vi % Cfg::kSlots;
             mbar_wait(bar(bars->kv_full[vs]), (vi / Cfg::kSlots) & 1, ab);
             const int lw = min(4, (rows + 31) >> 5);  // live warps per half
-            const int li = (half * lw + ((row >> 5))) * 32 + lane, ln = 64 * lw;
-            for (int e = li; e < 128 * Cfg::kBoxes * 8; e += ln) {
-              const int vr = e / (Cfg::kBoxes * 8), rest = e % (Cfg::kBoxes * 8);
-              if (vr >= keys_end || (vr < win_from && vr >= sink_end))
-                st_shared_v4(sKV + vs * Cfg::kTileBytes + (rest >> 3) * 16384 + vr * 128 + (rest & 7) * 16, 0u, 0u, 0u,
-                             0u);
-            }
+            const int li = (half * lw + (row >> 5)) * 32 + lane, chunk = li & (Cfg::kBoxes * 8 - 1);
+            const uint32_t to = sKV + vs * Cfg::kTileBytes + (chunk >> 3) * 16384 + (chunk & 7) * 16;
+            auto clear = [&](int from, int end) {
+              for (int vr = from + li / (Cfg::kBoxes * 8); vr < end; vr += 64 * lw / (Cfg::kBoxes * 8))
+                st_shared_v4(to + vr * 128, 0u, 0u, 0u, 0u);
+            };
+            const int end = max(0, min(128, keys_end));
+            clear(end, 128);
+            clear(max(0, sink_end), min(win_from, end));
             fence_proxy_async_smem();
           }
         }
@@ -712,11 +770,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       }
 
       // ---- epilogue: O / (sum of the weights applied) and the log-sum-exp, final or partial
-      const long long T = w.th * p.Hkv;
-      const int pe = (int)min((long long)p.pieces, T), piece = blockIdx.x;
-      const int pf = dec_piece_of(T, pe, w.start), pl = dec_piece_of(T, pe, w.start + w.keys.cnt - 1);
-      // slot of the block's partial in piece r: 2 r, or 2 r + 1 where an earlier block opens the piece
-      auto slot_of = [&](int r) { return 2 * r + (r == pf && dec_piece_lo(T, pe, pf) < w.start ? 1 : 0); };
+      const bool whole = w.whole();
+      const int slot = 2 * (int)blockIdx.x + (w.start > w.u0 ? 1 : 0);  // of its partial: the piece's first block, or a later one
       if (act) {
         mbar_wait(bar(bars->pv_done[t]), pvn & 1, ab);
         ++pvn;
@@ -733,8 +788,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         const bool dead = !(l_o > 0.0f) && l_o == l_o;  // no visible key (a NaN sum is not one)
         const long long tok = (long long)w.s.c0 + w.i0 + t * p.tq + tok_in_tile;
         const int head = w.h * p.G + head_in_group;
-        const long long prow = (long long)slot_of(piece) * (kTiles * 128) + t * 128 + row;
-        const long long o_size = (long long)p.total * p.Hq * D, part_size = 2LL * p.pieces * kTiles * 128 * D;
+        const long long ptile = (long long)slot * kTiles + t;
+        const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.pieces * kTiles * 128;
 #pragma unroll 1
         for (int cc = (D / 2) * half; cc < (D / 2) * (half + 1); cc += 32) {
           uint32_t o[32];
@@ -744,7 +799,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
           const float mul = l_o == l_o ? inv_l : l_o;
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = dead ? 0u : __float_as_uint(__uint_as_float(o[e]) * mul);
-          if (pf == pl) {
+          if (whole) {
             const long long oi = (tok * p.Hq + head) * D + cc;
             if (dbg_range(ab, oi, 32, o_size)) {
 #pragma unroll
@@ -757,16 +812,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
                 *reinterpret_cast<uint4*>(p.o + oi + e) = q;
               }
             }
-          } else if (dbg_range(ab, prow * D + cc, 32, part_size)) {
+          } else if (dbg_range(ab, ptile * 128 * D + (cc / 4 * 128 + row) * 4, 28 * 128 + 4, part_rows * D)) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(p.o_part + prow * D + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              reinterpret_cast<uint4*>(p.o_part + ptile * 128 * D)[(cc + e) / 4 * 128 + row] =
+                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
         if (mine && half == 0) {
           const long long li = (long long)head * p.total + tok;
-          if (pf != pl) {
-            if (dbg_range(ab, prow, 1, part_size / D)) p.lse_part[prow] = lse2;
+          if (!whole) {
+            if (dbg_range(ab, ptile * 128 + row, 1, part_rows)) p.lse_part[ptile * 128 + row] = lse2;
           } else if (dbg_range(ab, li, 1, (long long)p.Hq * p.total)) {
             p.lse[li] = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
           }
@@ -774,23 +830,28 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         tc_fence_before_sync();
       }
       vn += nv;
-      if (pf != pl && pf == piece)
-        split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * pl + (dec_piece_lo(T, pe, pf) < w.start ? 1 : 0));
+      if (!whole && w.start >= w.u0) {
+        const long long T = bars->th * p.Hkv;
+        const int last = ChunkSplit(T, chunk_pieces(p, T)).of(w.start + w.keys.cnt - 1);
+        split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * last + (slot & 1));
+      }
     }
     if (st == 0 && dbg_range(ab, blockIdx.x, 1, p.pieces)) p.split[blockIdx.x] = split;
-  } else if (warp >= 4) {
+  } else {
     if constexpr (kF8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kConvRegs) : "memory");
       // ---------------------------------------------------------------- E4M3 codes -> bf16 operand tiles
       constexpr int kPerRow = D / 16;  // 16-byte pieces of codes in a row
+      constexpr int kRowStep = Cfg::kConvThreads / kPerRow;
       const int ct = tid - 128 - Cfg::kSoftThreads;
-      const int c = ct % kPerRow;      // this thread's piece, in rows ct / kPerRow + k * (128 / kPerRow)
+      const int c = ct % kPerRow;      // this thread's piece, in rows ct / kPerRow + k * kRowStep
       const int box_shift = 31 - __clz(p.box_rows);
       uint32_t n = 0;
       Walk w;
       for (begin(w); w.valid(); w.next(p)) {
         for (int v = w.v0; v < w.v1; ++v) {
           const int key0 = w.keys.tile(v) * 128;
-  #pragma unroll 1
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const uint32_t rs = n % Cfg::kRawSlots, ks = n % Cfg::kSlots;
             mbar_wait(bar(bars->raw_full[rs]), (n / Cfg::kRawSlots) & 1, ab);
@@ -798,9 +859,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
             const uint8_t* raw = smem_gen + Cfg::kOffRaw + rs * Cfg::kRawSlotBytes;
             const uint8_t* scale = raw + Cfg::kRawBytes;
             const uint32_t dst = sKV + ks * Cfg::kTileBytes;
-  #pragma unroll 4
-            for (int k = 0; k < kPerRow; ++k) {
-              const int row = ct / kPerRow + k * (128 / kPerRow), key = key0 + row;
+#pragma unroll
+            for (int k = 0; k < 128 / kRowStep; ++k) {
+              const int row = ct / kPerRow + k * kRowStep, key = key0 + row;
               uint4 x = reinterpret_cast<const uint4*>(raw)[row * kPerRow + c];
               uint32_t s = scale[((row >> box_shift) << 7) + (row & (p.box_rows - 1))];
               // V rows that no row of the block sees may hold anything: 0 (their weights are 0)
@@ -811,14 +872,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
               const uint32_t f = (min(s, 134u) + 120u) << 7, ff = f | (f << 16);  // 2^(s - 127 + 120), bf16
               const uint32_t in[4] = {x.x, x.y, x.z, x.w};
               uint32_t r[8];
-  #pragma unroll
+#pragma unroll
               for (int e = 0; e < 4; ++e) {
                 r[2 * e] = mul_bf16x2(e4m3_pair_bits(__byte_perm(in[e], 0u, 0x1404)), ff);
                 r[2 * e + 1] = mul_bf16x2(e4m3_pair_bits(__byte_perm(in[e], 0u, 0x3424)), ff);
               }
               if (s > 134u) {  // scales above 2^7: a second factor; NaN for s = 255
                 const uint32_t g = s == (uint32_t)kScaleNan ? 0x7fc0u : (s - 134u + 127u) << 7;
-  #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 8; ++e) r[e] = mul_bf16x2(r[e], g | (g << 16));
               }
               // two 16-byte chunks; the upper half of a row's threads stores its odd chunk first,
@@ -853,29 +914,30 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
 }
 
 // Joins the blocks that are spread over several pieces: CTA (r, y) takes the block that starts in
-// piece r and goes on, if there is one, and of it the rows y, y + gridDim.y, ... (in groups). A row's
-// partials are weighted by 2^(their log-sum-exp - the largest), in piece order: the same sum in
-// every run. d / 4 threads per row, 16 bytes each; bound by the latency of the partials, which lie
-// in L2, so eight of them are in flight per thread. Launched as the main kernel's programmatic
-// dependent: it is resident by the time the last piece is written.
-constexpr int kMergeThreads = 256;
+// piece r and goes on, if there is one, and of it rows [8 y, 8 y + 8). A row's partials are
+// weighted by 2^(their log-sum-exp - the largest), in piece order: the same sum in every run. Bound
+// by the latency of the partials, which lie in L2, so eight of them are in flight per thread; the
+// rows leave through shared memory, whole. Launched as the main kernel's programmatic dependent: it
+// is resident by the time the last piece is written.
+constexpr int kMergeThreads = 256, kMergeRows = 8;
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const ChunkParams p, int tile_rows) {
-  constexpr int kLanes = D / 4, kRows = kMergeThreads / kLanes;
+__global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const ChunkParams p, int tiles) {
+  __shared__ uint2 sO[kMergeRows][D / 4 + 1];
   const Abort none{nullptr};
   griddep_wait();  // the pieces have been written
-  const int pf = blockIdx.x;
+  const int pf = blockIdx.x, tid = threadIdx.x;
   const int4 s = __ldcg(p.split + pf);
-  const int rows = s.y * p.G, pl = s.w >> 1;
-  const int c4 = (threadIdx.x % kLanes) * 4;
-  const long long part_rows = 2LL * p.pieces * tile_rows;
-  for (int first = blockIdx.y * kRows; first < rows; first += gridDim.y * kRows) {
-    const int rr = first + threadIdx.x / kLanes;
-    if (rr >= rows) break;
-    const int itok = rr / p.G, g = rr - itok * p.G, tile = itok >= p.tq ? 1 : 0;
-    const int srow = tile * 128 + rr - tile * p.tq * p.G;
-    auto prow_of = [&](int r) { return (2LL * r + (r == pf ? (s.w & 1) : 0)) * tile_rows + srow; };
-    if (!dbg_range(none, prow_of(pf), 1, part_rows) || !dbg_range(none, prow_of(pl), 1, part_rows)) break;
+  const int pl = s.w >> 1, first = blockIdx.y * kMergeRows, nrows = min(kMergeRows, s.y * p.G - first);
+  if (nrows <= 0) return;
+  const long long part_rows = 2LL * p.pieces * tiles * 128;
+  const int shift = nrows <= 1 ? 0 : 32 - __clz(nrows - 1);  // rows side by side: the next power of two
+  auto tile_of = [&](int r) { return (2LL * r + (r == pf ? (s.w & 1) : 0)) * tiles; };
+  for (int e = tid; e < (D / 4) << shift; e += kMergeThreads) {
+    const int rr = first + (e & ((1 << shift) - 1)), c4 = e >> shift;
+    if (rr - first >= nrows) continue;
+    const int itok = p.by_group(rr), tile = itok >= p.tq ? 1 : 0, srow = rr - tile * p.tq * p.G;
+    auto prow_of = [&](int r) { return (tile_of(r) + tile) * 128 + srow; };
+    if (!dbg_range(none, prow_of(pf), 1, part_rows) || !dbg_range(none, prow_of(pl), 1, part_rows)) continue;
     float mx = -INFINITY;
 #pragma unroll 8
     for (int r = pf; r <= pl; ++r) mx = fmaxf(mx, __ldcg(p.lse_part + prow_of(r)));
@@ -884,9 +946,9 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const Chu
     const float m_sub = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll 8
     for (int r = pf; r <= pl; ++r) {
-      const long long pr = prow_of(r);
-      const float wr = ex2_approx(__ldcg(p.lse_part + pr) - m_sub);
-      const float4 o4 = __ldcg(reinterpret_cast<const float4*>(p.o_part + pr * D + c4));
+      const float wr = ex2_approx(__ldcg(p.lse_part + prow_of(r)) - m_sub);
+      const float4 o4 = __ldcg(reinterpret_cast<const float4*>(p.o_part + (tile_of(r) + tile) * 128 * D) +
+                               c4 * 128 + srow);
       wsum += wr;
       acc.x = fmaf(wr, o4.x, acc.x);
       acc.y = fmaf(wr, o4.y, acc.y);
@@ -894,15 +956,16 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const Chu
       acc.w = fmaf(wr, o4.w, acc.w);
     }
     const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
-    const long long tok = (long long)s.x + itok;
-    const int head = s.z * p.G + g;
-    const long long oi = (tok * p.Hq + head) * D + c4;
-    if (dbg_range(none, oi, 4, (long long)p.total * p.Hq * D))
-      *reinterpret_cast<uint2*>(p.o + oi) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    const long long li = (long long)head * p.total + tok;
+    sO[rr - first][c4] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    const long long li = (long long)(s.z * p.G + rr - itok * p.G) * p.total + s.x + itok;
     if (c4 == 0 && dbg_range(none, li, 1, (long long)p.Hq * p.total))
       p.lse[li] = wsum == 0.0f ? -INFINITY : (m_sub + lg2_approx(wsum)) * kLn2;
+  }
+  __syncthreads();
+  for (int e = tid; e < nrows * (D / 4); e += kMergeThreads) {
+    const int rr = e / (D / 4), c4 = e % (D / 4), itok = p.by_group(first + rr);
+    const long long oi = ((long long)(s.x + itok) * p.Hq + s.z * p.G + first + rr - itok * p.G) * D + c4 * 4;
+    if (dbg_range(none, oi, 4, (long long)p.total * p.Hq * D)) *reinterpret_cast<uint2*>(p.o + oi) = sO[rr][c4];
   }
 }
 

@@ -433,21 +433,35 @@ def attention_bwd_varlen(q, k, v, o, lse, do, cu_seqlens, scale=None, causal=Fal
 # ---------------------------------------------------------------- paged caches: ragged chunks
 
 
-def _on_device(t: torch.Tensor):
-    """Context that makes the tensor's device current (the C layer launches on the current device)."""
-    if not t.is_cuda:
+def _cuda_index(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device (there is no CPU path)")
-    return torch.cuda.device(t.device)
+    return index
 
 
-def _check_rows(t: torch.Tensor, name: str, heads: int | None = None, d: int | None = None) -> int:
-    """Packed rows (total, heads, d) bf16, each row contiguous and 16-byte aligned; the rows may be slices of
-    a wider tensor. Returns the elements from one row to the next."""
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise ValueError(f"{name} must be a (total, heads, head_dim) bfloat16 CUDA tensor")
+def _launch(name: str, index: int, stream, *args) -> None:
+    """Call the C function on device `index` (it launches on the current device), on `stream` or that
+    device's current one."""
+    fn = getattr(load(), name)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != FA_OK:
+        _raise(status, name)
+
+
+def _check_rows(t: torch.Tensor, name: str, index: int, heads: int | None, d: int) -> int:
+    """Packed rows (total, heads, d) bf16 on device `index`, each row contiguous and 16-byte aligned; the rows
+    may be slices of a wider tensor. Returns the elements from one row to the next."""
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.get_device() != index:
+        raise ValueError(f"{name} must be a (total, heads, head_dim) bfloat16 tensor, on the other tensors' CUDA device")
     total, h, dim = t.shape
-    if (heads is not None and h != heads) or (d is not None and dim != d):
-        raise ValueError(f"{name} must be (total, {heads}, {d}) (got {tuple(t.shape)})")
+    if (heads is not None and h != heads) or dim != d:
+        raise ValueError(f"{name} must be (total, {heads or 'heads'}, {d}) (got {tuple(t.shape)})")
     s0, s1, s2 = t.stride()
     if total <= 1:
         s0 = h * dim
@@ -456,35 +470,40 @@ def _check_rows(t: torch.Tensor, name: str, heads: int | None = None, d: int | N
     return s0
 
 
-def _check_cache(like: torch.Tensor, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens):
-    """Pages, scales, block table, lengths and offsets of a ragged batch; returns (B, H, d, num_pages,
-    page_size, max_pages, k_scale pointer, v_scale pointer)."""
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _check_cache(index: int, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens):
+    """Pages, scales, block table, lengths and offsets of a ragged batch on device `index`; returns (B, H, d,
+    num_pages, page_size, max_pages, k_scale pointer, v_scale pointer)."""
     quantised = k_scale is not None
     if quantised != (v_scale is not None):
         raise ValueError("give both k_scale and v_scale (E4M3 pages), or neither (bfloat16 pages)")
-    kinds = (torch.float8_e4m3fn, torch.uint8) if quantised else (torch.bfloat16,)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    kinds = _E4M3 if quantised else (torch.bfloat16,)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must be (num_pages, page_size, heads, head_dim), of equal shape")
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype not in kinds or not t.is_contiguous() or t.device != like.device:
+        if t.dtype not in kinds or not t.is_contiguous() or t.get_device() != index:
             raise ValueError(f"{name} must be contiguous, on the rows' device and {' or '.join(map(str, kinds))} "
                              f"({'with' if quantised else 'without'} scales)")
-    num_pages, page_size, H, d = k_cache.shape
+    num_pages, page_size, H, d = shape
+    ks = vs = None
     if quantised:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or not t.is_contiguous() or \
-                    t.device != like.device or tuple(t.shape) != (num_pages, H, page_size):
+            if t.dtype not in _E8M0 or not t.is_contiguous() or t.get_device() != index or \
+                    t.shape != (num_pages, H, page_size):
                 raise ValueError(f"{name} must be a contiguous (num_pages, heads, page_size) tensor of E8M0 bytes "
                                  "(uint8 or float8_e8m0fnu) on the rows' device")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     for t, name in ((block_table, "block_table"), (seqlens, "seqlens"), (cu_seqlens, "cu_seqlens")):
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != like.device:
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.get_device() != index:
             raise ValueError(f"{name} must be a contiguous int32 tensor on the rows' device")
     B = seqlens.numel()
-    if seqlens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B or \
-            tuple(cu_seqlens.shape) != (B + 1,):
+    if seqlens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B or cu_seqlens.shape != (B + 1,):
         raise ValueError("block_table must be (B, max_pages), seqlens (B,) and cu_seqlens (B + 1,)")
-    return (B, H, d, num_pages, page_size, block_table.shape[1], k_scale.data_ptr() if quantised else None,
-            v_scale.data_ptr() if quantised else None)
+    return B, H, d, num_pages, page_size, block_table.shape[1], ks, vs
 
 
 def cache_write_paged(k_new, v_new, k_cache, v_cache, block_table, seqlens, cu_seqlens, k_scale=None, v_scale=None,
@@ -494,55 +513,63 @@ def cache_write_paged(k_new, v_new, k_cache, v_cache, block_table, seqlens, cu_s
     cu_seqlens[B] on are not read. k_cache, v_cache: (num_pages, page_size, H, d) bf16, or E4M3
     (float8_e4m3fn or uint8) with k_scale, v_scale (num_pages, H, page_size) E8M0 bytes (uint8 or
     float8_e8m0fnu): then each (token, head) row is quantised with its own power-of-two scale."""
-    with _on_device(k_new):
-        B, H, d, num_pages, page_size, max_pages, ks, vs = _check_cache(k_new, k_cache, v_cache, k_scale, v_scale,
-                                                                        block_table, seqlens, cu_seqlens)
-        stride = _check_rows(k_new, "k_new", H, d)
-        if v_new.shape != k_new.shape or v_new.device != k_new.device or _check_rows(v_new, "v_new", H, d) != stride:
-            raise ValueError("v_new must have the shape, device and row stride of k_new")
-        st = load().fa_cache_write(k_new.data_ptr(), v_new.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(),
-                                   ks, vs, block_table.data_ptr(), seqlens.data_ptr(), cu_seqlens.data_ptr(), B,
-                                   k_new.shape[0], H, d, num_pages, page_size, max_pages, _stream_handle(stream))
-        _raise(st, "fa_cache_write")
+    index = _cuda_index(k_new)
+    B, H, d, num_pages, page_size, max_pages, ks, vs = _check_cache(index, k_cache, v_cache, k_scale, v_scale,
+                                                                    block_table, seqlens, cu_seqlens)
+    stride = _check_rows(k_new, "k_new", index, H, d)
+    if v_new.shape != k_new.shape or _check_rows(v_new, "v_new", index, H, d) != stride:
+        raise ValueError("v_new must have the shape and row stride of k_new")
+    _launch("fa_cache_write", index, stream, k_new.data_ptr(), v_new.data_ptr(), stride, k_cache.data_ptr(),
+            v_cache.data_ptr(), ks, vs, block_table.data_ptr(), seqlens.data_ptr(), cu_seqlens.data_ptr(), B,
+            k_new.shape[0], H, d, num_pages, page_size, max_pages)
 
 
 def cache_read_paged_into(k_cache, v_cache, block_table, seqlens, cu_seqlens, k, v, k_scale=None, v_scale=None,
                           stream=None) -> None:
     """fa_cache_read: read the rows that cache_write_paged would write back into k, v (total, H, d) bf16,
     exactly; rows from cu_seqlens[B] on are left as they were."""
-    with _on_device(k):
-        B, H, d, num_pages, page_size, max_pages, ks, vs = _check_cache(k, k_cache, v_cache, k_scale, v_scale,
-                                                                        block_table, seqlens, cu_seqlens)
-        stride = _check_rows(k, "k", H, d)
-        if v.shape != k.shape or v.device != k.device or _check_rows(v, "v", H, d) != stride:
-            raise ValueError("v must have the shape, device and row stride of k")
-        st = load().fa_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(),
-                                  seqlens.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), stride, B,
-                                  k.shape[0], H, d, num_pages, page_size, max_pages, _stream_handle(stream))
-        _raise(st, "fa_cache_read")
+    index = _cuda_index(k)
+    B, H, d, num_pages, page_size, max_pages, ks, vs = _check_cache(index, k_cache, v_cache, k_scale, v_scale,
+                                                                    block_table, seqlens, cu_seqlens)
+    stride = _check_rows(k, "k", index, H, d)
+    if v.shape != k.shape or _check_rows(v, "v", index, H, d) != stride:
+        raise ValueError("v must have the shape and row stride of k")
+    _launch("fa_cache_read", index, stream, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(),
+            seqlens.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), stride, B, k.shape[0], H, d,
+            num_pages, page_size, max_pages)
 
 
 def cache_read_paged(k_cache, v_cache, block_table, seqlens, cu_seqlens, total, k_scale=None, v_scale=None,
                      stream=None):
     """cache_read_paged_into new tensors: returns (k, v), (total, H, d) bf16 (rows from cu_seqlens[B] on,
     if total is larger, are not initialised)."""
-    H, d = k_cache.shape[2:]
-    k, v = (_empty(stream, (total, H, d), torch.bfloat16, k_cache.device) for _ in range(2))
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be (num_pages, page_size, heads, head_dim), of equal shape")
+    k = k_cache.new_empty((total, *k_cache.shape[2:]), dtype=torch.bfloat16)
+    v = torch.empty_like(k)
+    _used_on(stream, k, v)
     cache_read_paged_into(k_cache, v_cache, block_table, seqlens, cu_seqlens, k, v, k_scale, v_scale, stream)
     return k, v
 
 
-def _empty(stream, shape, dtype, device) -> torch.Tensor:
-    """A new tensor that a kernel on `stream` (None: the current one) may use until it is done."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.is_cuda:
-        t.record_stream(stream)
-    return t
+def _used_on(stream, *new: torch.Tensor) -> None:
+    """Tensors made here are not handed out again before work on `stream` (None: the current one) is done."""
+    if stream is not None:
+        for t in new:
+            if t.is_cuda:
+                t.record_stream(stream)
 
 
 def chunk_workspace_bytes(B: int, total: int, Hq: int, Hkv: int, d: int) -> int:
     """Bytes of workspace chunk_paged_into uses on the current device."""
     return int(load().fa_chunk_workspace_bytes(B, total, Hq, Hkv, d))
+
+
+def _chunk_workspace(index: int, *sizes: int) -> int:
+    if index == torch.cuda.current_device():
+        return chunk_workspace_bytes(*sizes)
+    with torch.cuda.device(index):
+        return chunk_workspace_bytes(*sizes)
 
 
 def chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, lse, scale=None, causal=False,
@@ -551,31 +578,27 @@ def chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, l
     cu_seqlens[B] on are left as they were. Arguments as attention_chunk_paged; ``workspace``: a uint8 CUDA
     tensor of chunk_workspace_bytes(B, total, Hq, Hkv, d) bytes (any contents; calls that may overlap need
     workspaces of their own), or None to allocate one."""
-    with _on_device(q):
-        B, Hkv, d, num_pages, page_size, max_pages, ks, vs = _check_cache(q, k_cache, v_cache, k_scale, v_scale,
-                                                                          block_table, seqlens, cu_seqlens)
-        stride = _check_rows(q, "q", None, d)
-        total, Hq, _ = q.shape
-        if o.shape != q.shape or o.dtype != torch.bfloat16 or o.device != q.device or not o.is_contiguous():
-            raise ValueError("o must be a contiguous bfloat16 tensor of q's shape on its device")
-        _check_lse(lse, (Hq, total))
-        if lse.device != q.device:
-            raise ValueError("lse must be on q's device")
-        if Hq == 0 or Hq % Hkv:
-            raise ValueError(f"the {Hq} query heads must be a multiple of the cache's {Hkv}")
-        if workspace is None:
-            own = torch.empty(chunk_workspace_bytes(B, total, Hq, Hkv, d), dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                own.record_stream(stream)
-            ws, wb = own.data_ptr(), own.numel()
-        else:
-            ws, wb = _check_workspace(workspace)
-        st = load().fa_chunk_paged(q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
-                                   block_table.data_ptr(), seqlens.data_ptr(), cu_seqlens.data_ptr(), o.data_ptr(),
-                                   lse.data_ptr(), B, total, Hq, Hkv, d, num_pages, page_size, max_pages,
-                                   _scale(scale, d), int(bool(causal)), int(window[0]), int(window[1]), int(sinks),
-                                   ws, wb, _stream_handle(stream))
-        _raise(st, "fa_chunk_paged")
+    index = _cuda_index(q)
+    B, Hkv, d, num_pages, page_size, max_pages, ks, vs = _check_cache(index, k_cache, v_cache, k_scale, v_scale,
+                                                                      block_table, seqlens, cu_seqlens)
+    stride = _check_rows(q, "q", index, None, d)
+    total, Hq, _ = q.shape
+    if o.shape != q.shape or o.dtype != torch.bfloat16 or o.get_device() != index or not o.is_contiguous():
+        raise ValueError("o must be a contiguous bfloat16 tensor of q's shape on its device")
+    if lse.shape != (Hq, total) or lse.dtype != torch.float32 or lse.get_device() != index or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous ({Hq}, {total}) float32 tensor on q's device")
+    if Hq == 0 or Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"the {Hq} query heads must be a multiple of the cache's {Hkv}")
+    if workspace is None:
+        workspace = o.new_empty(_chunk_workspace(index, B, total, Hq, Hkv, d), dtype=torch.uint8)
+        _used_on(stream, workspace)
+    elif workspace.get_device() != index:
+        raise ValueError("workspace must be on q's device")
+    ws, wb = _check_workspace(workspace)
+    _launch("fa_chunk_paged", index, stream, q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
+            block_table.data_ptr(), seqlens.data_ptr(), cu_seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, total, Hq,
+            Hkv, d, num_pages, page_size, max_pages, _scale(scale, d), 1 if causal else 0, int(window[0]),
+            int(window[1]), int(sinks), ws, wb)
 
 
 def attention_chunk_paged(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, scale=None, causal=False,
@@ -587,8 +610,11 @@ def attention_chunk_paged(q, k_cache, v_cache, block_table, seqlens, cu_seqlens,
     seqlens[b] keys; query head h reads cache head h // (Hq // Hkv). Pages and scales as in cache_write_paged.
     ``window``: (left, right) as everywhere; ``sinks``: a sequence's first keys that stay visible left of the
     window. Rows from cu_seqlens[B] on are not initialised (chunk_paged_into leaves them as they were)."""
-    o = _empty(stream, q.shape, torch.bfloat16, q.device)
-    lse = _empty(stream, (q.shape[1], q.shape[0]), torch.float32, q.device)
+    if q.dim() != 3:
+        raise ValueError("q must be a (total, heads, head_dim) bfloat16 CUDA tensor")
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = q.new_empty((q.shape[1], q.shape[0]), dtype=torch.float32)
+    _used_on(stream, o, lse)
     chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, lse, scale, causal, window, sinks,
                      k_scale, v_scale, None, stream)
     return o, lse

@@ -67,10 +67,6 @@ struct ChunkParams {
                            // (0: none), head, 2 * last piece + (slot of piece r is 2 r + 1)
 };
 
-#ifndef FA_S
-#define FA_S (kTiles == 2 ? 2 : 2)
-#define FA_R (kTiles == 2 ? 5 : 7)
-#endif
 template <int D, bool kF8, int kTiles>
 struct ChunkCfg {
   static constexpr int kSoftWarps = 8 * kTiles;       // row split: two warps per 32 rows
@@ -86,8 +82,8 @@ struct ChunkCfg {
   static constexpr int kTileBytes = 128 * D * 2;      // a bf16 tile of Q, K or V
   static constexpr int kRawBytes = 128 * D;           // the codes of a K or V tile
   static constexpr int kRawSlotBytes = kRawBytes + 1024;  // codes, then the scales of each page box at 128 bytes
-  static constexpr int kSlots = kF8 ? (D == 64 ? 4 : FA_S) : (D == 64 ? 10 : kTiles == 2 ? 4 : 5);
-  static constexpr int kRawSlots = kF8 ? (D == 64 ? (kTiles == 2 ? 12 : 14) : FA_R) : 0;
+  static constexpr int kSlots = kF8 ? (D == 64 ? 5 : 3) : (D == 64 ? 10 : kTiles == 2 ? 4 : 5);
+  static constexpr int kRawSlots = kF8 ? (D == 64 ? 9 : kTiles == 2 ? 3 : 5) : 0;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = kTiles * kTileBytes;
   static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
@@ -103,21 +99,6 @@ struct ChunkCfg {
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
-template <class Cfg>
-struct ChunkBars {
-  uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[Cfg::kSlots], kv_empty[Cfg::kSlots];
-  uint64_t raw_full[Cfg::kRawSlots + 1], raw_empty[Cfg::kRawSlots + 1];
-  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t mma_done;
-  uint32_t tmem_base;
-  int abort_flag;
-  long long u0, u1, th;     // the piece, the length of one head's list
-  long long first_start;    // the piece's first block: its position on the list of all heads
-  int first_h, first_b, first_blk;
-  long long sums[2][4];     // scans
-};
-
 // A sequence: first packed row, rows and keys. Offsets or lengths out of range make it empty
 // (reported by report_bad_batch).
 struct ChunkSeq {
@@ -131,6 +112,23 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b) {
   s.n = (n < 0 || n > (long long)p.max_pages * p.page_size) ? 0 : n;
   return s;
 }
+
+template <class Cfg>
+struct ChunkBars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[Cfg::kSlots], kv_empty[Cfg::kSlots];
+  uint64_t raw_full[Cfg::kRawSlots + 1], raw_empty[Cfg::kRawSlots + 1];
+  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  long long u0, u1, th;     // the piece, the length of one head's list
+  long long first_start;    // the piece's first block: its position on the list of all heads
+  int first_h, first_b, first_blk;
+  ChunkSeq first_seq;
+  long long sums[3][4];     // scans
+  int many[4];
+};
 
 // Keys visible to some row of a block, and the tiles that hold them: tile v of the block is key
 // tile v for v < ns (sinks left of the window), lo + v - ns from there on; cnt >= 1 in all (a
@@ -189,7 +187,7 @@ struct ChunkWalk {
     h = bars->first_h;
     b = bars->first_b;
     blk = bars->first_blk;
-    s = chunk_seq(p, b);
+    s = bars->first_seq;
     set(p);
   }
   __device__ __forceinline__ void next(const ChunkParams& p) {
@@ -228,13 +226,6 @@ struct ChunkSplit {
   }
 };
 
-// Pieces of a list of T tiles: with less than kMinPiece tiles each, CTAs would spend more time on
-// setting up and joining than on tiles.
-constexpr int kMinPiece = 2;
-__device__ __forceinline__ int chunk_pieces(const ChunkParams& p, long long T) {
-  return (int)min((long long)p.pieces, max(1LL, T / kMinPiece));
-}
-
 // The set-up of one CTA by 128 threads (tid 0..127 here): which piece is its own, and where the
 // piece's first block lies. Blocks are counted per run of sequences, then key tiles per run of
 // blocks. (All the CTA's warps used to take part: what bounds this is the issue of its
@@ -259,27 +250,45 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, Bars* bars, int
   const int rb0 = min(p.B, tid * run), rb1 = min(p.B, rb0 + run);
   const int tokens = kTiles * p.tq;
   auto blocks_of = [&](const ChunkSeq& s) { return p.by_tokens(s.rows + tokens - 1); };
-  long long blocks = 0, nb;
-  for (int b = rb0; b < rb1; ++b) blocks += blocks_of(chunk_seq(p, b));
-  const long long blocks_incl = plan_scan(blocks, bars->sums[0], tid, nb);
-  run_base[tid] = (int)(blocks_incl - blocks);
-  named_bar_sync(1, kPlanThreads);
-  // this thread's blocks [q0, q1): found by the run of sequences that holds q0
-  const long long each = (nb + kPlanThreads - 1) / kPlanThreads;
-  const long long q0 = min(nb, each * tid), q1 = min(nb, q0 + each);
-  int b = 0, blk = 0;
-  if (q0 < q1) {
-    int lo = 0;
-#pragma unroll
-    for (int step = kPlanThreads / 2; step > 0; step >>= 1)
-      if (run_base[lo + step] <= q0) lo += step;
-    b = lo * run;
-    blk = (int)(q0 - run_base[lo]);
+  auto tiles_of = [&](const ChunkSeq& s, int blk) {
+    const int i0 = blk * tokens, pos0 = s.n - s.rows + i0;
+    return chunk_keys(p, s.n, pos0, pos0 + min(tokens, s.rows - i0) - 1).cnt;
+  };
+  // Few blocks per run (decoding steps, short chunks): their tiles are counted at once.
+  constexpr int kFew = 4;
+  long long blocks = 0, tiles = 0, nb, th;
+  for (int b = rb0; b < rb1; ++b) {
+    const ChunkSeq s = chunk_seq(p, b);
+    const int m = blocks_of(s);
+    blocks += m;
+    for (int k = 0; k < m && blocks <= kFew; ++k) tiles += tiles_of(s, k);
   }
-  // visit the thread's blocks in order; f(b, blk, tiles of the block) until it returns false
+  const bool many = __any_sync(0xffffffffu, blocks > kFew);
+  if ((tid & 31) == 0) bars->many[tid >> 5] = many;
+  long long incl = plan_scan(tiles, bars->sums[0], tid, th);
+  int b = rb0, blk = 0;      // this thread's first block, and how many it has
+  long long mine = blocks;
+  if (bars->many[0] | bars->many[1] | bars->many[2] | bars->many[3]) {
+    // The blocks of all sequences are dealt out evenly; a thread's first is found by the run that holds it.
+    const long long blocks_incl = plan_scan(blocks, bars->sums[1], tid, nb);
+    run_base[tid] = (int)(blocks_incl - blocks);
+    named_bar_sync(1, kPlanThreads);
+    const long long each = (nb + kPlanThreads - 1) / kPlanThreads;
+    const long long q0 = min(nb, each * tid);
+    mine = min(nb, q0 + each) - q0;
+    if (mine > 0) {
+      int lo = 0;
+#pragma unroll
+      for (int step = kPlanThreads / 2; step > 0; step >>= 1)
+        if (run_base[lo + step] <= q0) lo += step;
+      b = min(lo * run, p.B - 1);
+      blk = (int)(q0 - run_base[lo]);
+    }
+  }
+  // visit the thread's blocks in order; f(sequence, block, its rows and keys, tiles) until it returns false
   auto visit = [&](auto f) {
     int bb = b, kk = blk;
-    for (long long q = q0; q < q1;) {
+    for (long long q = 0; q < mine && bb < p.B;) {
       const ChunkSeq s = chunk_seq(p, bb);
       const int nbb = blocks_of(s);
       if (kk >= nbb) {
@@ -287,20 +296,22 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, Bars* bars, int
         ++bb;
         continue;
       }
-      const int i0 = kk * tokens, pos0 = s.n - s.rows + i0;
-      if (!f(bb, kk, chunk_keys(p, s.n, pos0, pos0 + min(tokens, s.rows - i0) - 1).cnt)) return;
+      if (!f(bb, kk, s, tiles_of(s, kk))) return;
       ++kk;
       ++q;
     }
   };
-  long long tiles = 0, th;
-  visit([&](int, int, int cnt) {
-    tiles += cnt;
-    return true;
-  });
-  const long long tiles_incl = plan_scan(tiles, bars->sums[1], tid, th), excl = tiles_incl - tiles;
+  if (bars->many[0] | bars->many[1] | bars->many[2] | bars->many[3]) {
+    tiles = 0;
+    visit([&](int, int, const ChunkSeq&, int cnt) {
+      tiles += cnt;
+      return true;
+    });
+    incl = plan_scan(tiles, bars->sums[2], tid, th);
+  }
+  const long long excl = incl - tiles;
   const long long T = th * p.Hkv;
-  const int pe = chunk_pieces(p, T), r = blockIdx.x;
+  const int pe = (int)min((long long)p.pieces, T), r = blockIdx.x;
   long long u0 = T, u1 = T;
   if (r < pe && T > 0) {
     const ChunkSplit split(T, pe);
@@ -316,9 +327,9 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, Bars* bars, int
   if (u0 >= u1) return;
   const int h = u0 < (1LL << 31) && th < (1LL << 31) ? (int)((unsigned)u0 / (unsigned)th) : (int)(u0 / th);
   const long long w0 = u0 - (long long)h * th;
-  if (excl <= w0 && w0 < tiles_incl) {
+  if (excl <= w0 && w0 < incl) {
     long long at = excl;
-    visit([&](int bb, int kk, int cnt) {
+    visit([&](int bb, int kk, const ChunkSeq& s, int cnt) {
       if (w0 >= at + cnt) {
         at += cnt;
         return true;
@@ -326,6 +337,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, Bars* bars, int
       bars->first_h = h;
       bars->first_b = bb;
       bars->first_blk = kk;
+      bars->first_seq = s;
       bars->first_start = at + (long long)h * th;
       return false;
     });
@@ -500,7 +512,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       }
     };
     int page = 0, row = 0;
-    if (w.valid()) place(w, w.v0, page, row);
     for (; w.valid() && !ab.raised();) {
       const int nact = (kTiles == 2 && w.ntok > p.tq) ? 2 : 1;
       if (lane == 0) {
@@ -520,6 +531,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         }
       }
       __syncwarp();
+      place(w, w.v0, page, row);
       const int h = w.h;
       for (int v = w.v0; v < w.v1 && !ab.raised(); ++v) {
         const int pg = page, rw = row;
@@ -553,7 +565,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         }
       }
       w.next(p);
-      if (w.valid()) place(w, w.v0, page, row);
     }
     // every load issued lands before the CTA exits
     for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
@@ -612,14 +623,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         mma_commit(bar(bars->kv_empty[ks]));
         for (int v = 0; v < nv; ++v) {
           const bool more = v + 1 < nv;
-          const uint32_t vs = kv_wait(kvn + 1);
-          kvn += 2;
-          if (more) ks = kv_wait(kvn);
+          uint32_t vs = 0;
+          if (more) ks = kv_wait(kvn + 2);
           for (int t = 0; t < nact; ++t) {
             if (more) issue_s(t, ks, v + 2 == nv);
             if (more && t == nact - 1) mma_commit(bar(bars->kv_empty[ks]));
+            if (t == 0) vs = kv_wait(kvn + 1);
             issue_pv(t, vs, v == 0);
           }
+          kvn += 2;
           mma_commit(bar(bars->kv_empty[vs]));
         }
       }
@@ -832,7 +844,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       vn += nv;
       if (!whole && w.start >= w.u0) {
         const long long T = bars->th * p.Hkv;
-        const int last = ChunkSplit(T, chunk_pieces(p, T)).of(w.start + w.keys.cnt - 1);
+        const int last = ChunkSplit(T, (int)min((long long)p.pieces, T)).of(w.start + w.keys.cnt - 1);
         split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * last + (slot & 1));
       }
     }

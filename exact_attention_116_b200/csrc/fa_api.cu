@@ -18,6 +18,7 @@
 #include "fa_bwd_dq.cuh"
 #include "fa_cache.cuh"
 #include "fa_chunk.cuh"
+#include "fa_chunk_few.cuh"
 #include "fa_decode.cuh"
 #include "fa_fwd.cuh"
 
@@ -96,7 +97,9 @@ bool chunk_attribute() {
 
 template <int D>
 bool chunk_attributes() {
-  return chunk_attribute<D, false, 1>() && chunk_attribute<D, false, 2>() && chunk_attribute<D, true, 1>() &&
+  return cudaFuncSetAttribute(fa::fa_chunk_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fa::FewCfg::kSmemBytes) == cudaSuccess &&
+         chunk_attribute<D, false, 1>() && chunk_attribute<D, false, 2>() && chunk_attribute<D, true, 1>() &&
          chunk_attribute<D, true, 2>();
 }
 
@@ -647,15 +650,15 @@ int make_map_chunk_q(CUtensorMap* m, const void* q, int total, int Hkv, int G, i
 }
 
 // Pages (num_pages, page_size, H, d): box_rows rows of one head, 64 bf16 columns (swizzled) or all
-// d codes of E4M3 pages (as they lie).
+// d codes of E4M3 pages (as they lie, or swizzled for the tensor core).
 int make_map_pages(CUtensorMap* m, const void* base, int num_pages, int page_size, int H, int d, int box_rows,
-                   bool f8) {
+                   bool f8, bool swizzle) {
   const cuuint64_t e = f8 ? 1 : 2;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)page_size, (cuuint64_t)num_pages};
   const cuuint64_t strides[3] = {d * e, (cuuint64_t)H * d * e, (cuuint64_t)page_size * H * d * e};
   const cuuint32_t box[4] = {f8 ? (cuuint32_t)d : 64u, 1, (cuuint32_t)box_rows, 1};
   return encode_map(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides,
-                    box, f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+                    box, f8 && !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Scales (num_pages * H, page_size): box_rows consecutive keys of one head.
@@ -676,6 +679,13 @@ fa::FastDiv fast_div(unsigned d) {
   return {(unsigned)((((1ull << 32) << s) + d - 1) / d - (1ull << 32)), s};
 }
 
+// Rows of a few tokens over E4M3 pages take the transposed kernel: when a sequence's rows fit its
+// 16-row blocks on average (a longer chunk in such a batch is cut into several, which read its keys
+// again).
+bool chunk_few(bool f8, int d, int B, int total, int G) {
+  return f8 && d == fa::kFewD && G <= fa::kFewRows && (double)total <= (double)B * (fa::kFewRows / G);
+}
+
 struct ChunkWorkspace {
   size_t o_bytes, lse_bytes, split_bytes;
   size_t bytes() const { return o_bytes + lse_bytes + split_bytes; }
@@ -693,11 +703,11 @@ int chunk_launch(int grid, const CUtensorMap* m, const fa::ChunkParams& p, cudaS
 }
 
 // The join of blocks that are spread over several pieces, as the main kernel's programmatic dependent.
-template <int D>
-int chunk_merge_launch(int pieces, int tiles, const fa::ChunkParams& p, cudaStream_t stream) {
-  const long long rows = std::min<long long>((long long)p.total * p.G, tiles * 128);
+template <int D, int kTiles>
+int chunk_merge_launch(int pieces, const fa::ChunkParams& p, cudaStream_t stream) {
+  const long long rows = std::min<long long>((long long)p.total * p.G, kTiles * 128);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pieces, (unsigned)((rows + fa::kMergeRows - 1) / fa::kMergeRows));
+  cfg.gridDim = dim3(pieces, (unsigned)((rows + fa::merge_rows(kTiles) - 1) / fa::merge_rows(kTiles)));
   cfg.blockDim = dim3(fa::kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -705,7 +715,7 @@ int chunk_merge_launch(int pieces, int tiles, const fa::ChunkParams& p, cudaStre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fa::fa_chunk_merge_kernel<D>, p, tiles) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, fa::fa_chunk_merge_kernel<D, kTiles>, p) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
@@ -1082,7 +1092,8 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   int dev, sms;
   if ((st = device_setup(&dev, &sms))) return st;
   if (total == 0) return FA_OK;
-  const int tiles = chunk_tiles(B, total, G), tq = 128 / G;
+  const bool few = chunk_few(f8, d, B, total, G);
+  const int tiles = chunk_tiles(B, total, G), tq = (few ? fa::kFewRows : 128) / G;
   const ChunkWorkspace wb = chunk_workspace(sms, tiles, d);
   if (workspace) {
     const Span ws{workspace, wb.bytes()};
@@ -1091,16 +1102,16 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
       return FA_ERR_INVALID_ARG;
   }
   // pieces: one per SM, and no more than the key tiles there can be
-  const double blocks = (double)(total / (tiles * tq)) + std::min(B, total);
+  const double blocks = (double)(total / ((few ? 1 : tiles) * tq)) + std::min(B, total);
   const int key_tiles = (max_keys + 127) / 128;
   const double most = blocks * Hkv * key_tiles;
-  const int pieces = most < sms ? (int)most : sms;
+  const int pieces = most < sms ? (int)most : std::min(sms, fa::kMergeMaxPieces);
   int box_rows = 16;
   while (box_rows < 128 && page_size % (2 * box_rows) == 0) box_rows *= 2;
   CUtensorMap m[5];
-  if ((st = make_map_chunk_q(&m[0], q, total, Hkv, G, d, q_stride, tq)) ||
-      (st = make_map_pages(&m[1], k_cache, num_pages, page_size, Hkv, d, box_rows, f8)) ||
-      (st = make_map_pages(&m[2], v_cache, num_pages, page_size, Hkv, d, box_rows, f8)))
+  if ((!few && (st = make_map_chunk_q(&m[0], q, total, Hkv, G, d, q_stride, tq))) ||
+      (st = make_map_pages(&m[1], k_cache, num_pages, page_size, Hkv, d, box_rows, f8, few)) ||
+      (st = make_map_pages(&m[2], v_cache, num_pages, page_size, Hkv, d, box_rows, f8, few)))
     return st;
   m[3] = m[1];
   m[4] = m[2];
@@ -1123,7 +1134,7 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   p.page_size = page_size;
   p.by_page = fast_div(page_size);
   p.by_group = fast_div(G);
-  p.by_tokens = fast_div(tiles * tq);
+  p.by_tokens = fast_div((few ? 1 : tiles) * tq);
   p.box_rows = box_rows;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
@@ -1141,12 +1152,19 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   p.lse_part = reinterpret_cast<float*>(static_cast<char*>(ws) + wb.o_bytes);
   p.split = reinterpret_cast<int4*>(static_cast<char*>(ws) + wb.o_bytes + wb.lse_bytes);
   if (log_enabled())
-    std::fprintf(stderr, "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d pieces=%d box=%d win=(%d,%d) sinks=%d\n",
-                 B, total, Hq, Hkv, d, f8, tiles, pieces, box_rows, win_l, win_r, sinks);
-  st = d == 64 ? chunk_variant<64>(f8, tiles, pieces, m, p, cs) : chunk_variant<128>(f8, tiles, pieces, m, p, cs);
+    std::fprintf(stderr, "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d few=%d pieces=%d box=%d win=(%d,%d) sinks=%d\n",
+                 B, total, Hq, Hkv, d, f8, tiles, few, pieces, box_rows, win_l, win_r, sinks);
+  if (few) {
+    fa::fa_chunk_few_kernel<<<pieces, fa::kFewThreads, fa::FewCfg::kSmemBytes, cs>>>(
+        m[1], m[2], m[3], m[4], static_cast<const __nv_bfloat16*>(q), q_stride, p);
+    st = launch_status();
+  } else {
+    st = d == 64 ? chunk_variant<64>(f8, tiles, pieces, m, p, cs) : chunk_variant<128>(f8, tiles, pieces, m, p, cs);
+  }
   // (with one key tile per block at most, or one piece, no block is spread over pieces)
   if (!st && pieces > 1 && key_tiles > 1)
-    st = d == 64 ? chunk_merge_launch<64>(pieces, tiles, p, cs) : chunk_merge_launch<128>(pieces, tiles, p, cs);
+    st = d == 64 ? (tiles == 1 ? chunk_merge_launch<64, 1>(pieces, p, cs) : chunk_merge_launch<64, 2>(pieces, p, cs))
+                 : (tiles == 1 ? chunk_merge_launch<128, 1>(pieces, p, cs) : chunk_merge_launch<128, 2>(pieces, p, cs));
   if (!workspace && cudaFreeAsync(ws, cs) != cudaSuccess && !st) st = FA_ERR_CUDA;
   return st;
 }

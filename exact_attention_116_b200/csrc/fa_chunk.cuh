@@ -623,15 +623,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         mma_commit(bar(bars->kv_empty[ks]));
         for (int v = 0; v < nv; ++v) {
           const bool more = v + 1 < nv;
-          uint32_t vs = 0;
-          if (more) ks = kv_wait(kvn + 2);
+          const uint32_t vs = kv_wait(kvn + 1);
+          kvn += 2;
+          if (more) ks = kv_wait(kvn);
           for (int t = 0; t < nact; ++t) {
             if (more) issue_s(t, ks, v + 2 == nv);
             if (more && t == nact - 1) mma_commit(bar(bars->kv_empty[ks]));
-            if (t == 0) vs = kv_wait(kvn + 1);
             issue_pv(t, vs, v == 0);
           }
-          kvn += 2;
           mma_commit(bar(bars->kv_empty[vs]));
         }
       }
@@ -926,52 +925,82 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
 }
 
 // Joins the blocks that are spread over several pieces: CTA (r, y) takes the block that starts in
-// piece r and goes on, if there is one, and of it rows [8 y, 8 y + 8). A row's partials are
-// weighted by 2^(their log-sum-exp - the largest), in piece order: the same sum in every run. Bound
-// by the latency of the partials, which lie in L2, so eight of them are in flight per thread; the
-// rows leave through shared memory, whole. Launched as the main kernel's programmatic dependent: it
-// is resident by the time the last piece is written.
-constexpr int kMergeThreads = 256, kMergeRows = 8;
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const ChunkParams p, int tiles) {
-  __shared__ uint2 sO[kMergeRows][D / 4 + 1];
+// piece r and goes on, if there is one, and of it kRows rows. A row's partials are weighted by
+// 2^(their log-sum-exp - the largest), in piece order: the same sum in every run. Bound by the
+// latency of the partials, which lie in L2: those of a row are read sixteen at a time, ahead of the
+// log-sum-exps that weigh them, which the CTA reads together. The rows leave through shared memory,
+// whole. Launched as the main kernel's programmatic dependent: an SM takes it as soon as its CTA of
+// the main kernel is done.
+constexpr int kMergeThreads = 256, kMergeMaxPieces = 192;
+constexpr __host__ __device__ int merge_rows(int tiles) { return tiles == 2 ? 32 : 8; }
+template <int D, int kTiles>
+__global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const ChunkParams p) {
+  constexpr int kRows = merge_rows(kTiles), kBatch = 16;
+  __shared__ uint2 sO[kRows][D / 4 + 1];
+  __shared__ float sL[kRows][kMergeMaxPieces];
   const Abort none{nullptr};
   griddep_wait();  // the pieces have been written
   const int pf = blockIdx.x, tid = threadIdx.x;
   const int4 s = __ldcg(p.split + pf);
-  const int pl = s.w >> 1, first = blockIdx.y * kMergeRows, nrows = min(kMergeRows, s.y * p.G - first);
+  const int m = (s.w >> 1) - pf + 1, first = blockIdx.y * kRows, nrows = min(kRows, s.y * p.G - first);
   if (nrows <= 0) return;
-  const long long part_rows = 2LL * p.pieces * tiles * 128;
+  if (!dbg_range(none, pf, m, p.pieces) || m > kMergeMaxPieces) return;
+  // 128-row tile of partials i of the block, for its rows of tile 0 or 1; row in the tile
+  auto tile_of = [&](int i, int t) { return ((2LL * (pf + i) + (i == 0 ? (s.w & 1) : 0)) * kTiles + t) * 128; };
+  auto locate = [&](int rr, int& t, int& srow) {
+    t = p.by_group(rr) >= p.tq ? 1 : 0;
+    srow = rr - t * p.tq * p.G;
+  };
   const int shift = nrows <= 1 ? 0 : 32 - __clz(nrows - 1);  // rows side by side: the next power of two
-  auto tile_of = [&](int r) { return (2LL * r + (r == pf ? (s.w & 1) : 0)) * tiles; };
-  for (int e = tid; e < (D / 4) << shift; e += kMergeThreads) {
+  const int items = (D / 4) << shift;
+  float4 o4[kBatch];
+  auto fetch = [&](int e, int from) {
     const int rr = first + (e & ((1 << shift) - 1)), c4 = e >> shift;
-    if (rr - first >= nrows) continue;
-    const int itok = p.by_group(rr), tile = itok >= p.tq ? 1 : 0, srow = rr - tile * p.tq * p.G;
-    auto prow_of = [&](int r) { return (tile_of(r) + tile) * 128 + srow; };
-    if (!dbg_range(none, prow_of(pf), 1, part_rows) || !dbg_range(none, prow_of(pl), 1, part_rows)) continue;
+    int t, srow;
+    locate(rr, t, srow);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (from + i < m && rr - first < nrows)
+        o4[i] = __ldcg(reinterpret_cast<const float4*>(p.o_part + tile_of(from + i, t) * D) + c4 * 128 + srow);
+  };
+  if (tid < items) fetch(tid, 0);
+  for (int e = tid; e < nrows * m; e += kMergeThreads) {
+    const int i = e / nrows, rr = e - i * nrows;
+    int t, srow;
+    locate(first + rr, t, srow);
+    sL[rr][i] = __ldcg(p.lse_part + tile_of(i, t) + srow);
+  }
+  __syncthreads();
+  for (int e = tid; e < items; e += kMergeThreads) {
+    const int rr = e & ((1 << shift) - 1), c4 = e >> shift;
+    if (e != tid) fetch(e, 0);
+    if (rr >= nrows) continue;
     float mx = -INFINITY;
-#pragma unroll 8
-    for (int r = pf; r <= pl; ++r) mx = fmaxf(mx, __ldcg(p.lse_part + prow_of(r)));
+    for (int i = 0; i < m; ++i) mx = fmaxf(mx, sL[rr][i]);
+    const float m_sub = mx == -INFINITY ? 0.0f : mx;
     float wsum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float m_sub = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll 8
-    for (int r = pf; r <= pl; ++r) {
-      const float wr = ex2_approx(__ldcg(p.lse_part + prow_of(r)) - m_sub);
-      const float4 o4 = __ldcg(reinterpret_cast<const float4*>(p.o_part + (tile_of(r) + tile) * 128 * D) +
-                               c4 * 128 + srow);
-      wsum += wr;
-      acc.x = fmaf(wr, o4.x, acc.x);
-      acc.y = fmaf(wr, o4.y, acc.y);
-      acc.z = fmaf(wr, o4.z, acc.z);
-      acc.w = fmaf(wr, o4.w, acc.w);
+    for (int from = 0; from < m; from += kBatch) {
+      if (from > 0) fetch(e, from);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (from + i >= m) continue;
+        const float w = ex2_approx(sL[rr][from + i] - m_sub);
+        wsum += w;
+        acc.x = fmaf(w, o4[i].x, acc.x);
+        acc.y = fmaf(w, o4[i].y, acc.y);
+        acc.z = fmaf(w, o4[i].z, acc.z);
+        acc.w = fmaf(w, o4[i].w, acc.w);
+      }
     }
     const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
-    sO[rr - first][c4] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    const long long li = (long long)(s.z * p.G + rr - itok * p.G) * p.total + s.x + itok;
-    if (c4 == 0 && dbg_range(none, li, 1, (long long)p.Hq * p.total))
-      p.lse[li] = wsum == 0.0f ? -INFINITY : (m_sub + lg2_approx(wsum)) * kLn2;
+    sO[rr][c4] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (c4 == 0) {
+      const int itok = p.by_group(first + rr);
+      const long long li = (long long)(s.z * p.G + first + rr - itok * p.G) * p.total + s.x + itok;
+      if (dbg_range(none, li, 1, (long long)p.Hq * p.total))
+        p.lse[li] = wsum == 0.0f ? -INFINITY : (m_sub + lg2_approx(wsum)) * kLn2;
+    }
   }
   __syncthreads();
   for (int e = tid; e < nrows * (D / 4); e += kMergeThreads) {

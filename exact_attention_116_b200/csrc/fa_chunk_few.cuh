@@ -1,0 +1,583 @@
+// Attention of a few new tokens over a paged E4M3 cache, for sm_100a: fa_chunk.cuh's operation, list
+// of key tiles, pieces and partials, for blocks of at most 16 rows (tokens times the query heads of
+// a key/value head) and d = 128: decoding steps.
+//
+// The codes go from the cache to the tensor core as they lie. Both products are transposed, so that
+// the cache is operand A and the few rows are its narrow partner:
+//   S^T (128 keys x 16 rows) = K Q^T,   O^T (128 columns x 16 rows) += V^T W^T.
+// A key is then a lane, and its scales, 2^ek and 2^ev, are scalars of the lane's thread:
+//   score(row, key) = S * 2^ek * scale,   W(row, key) = P(row, key) * 2^(ev - E).
+// Q and W are sums of three E5M2 numbers, each the remainder of the ones before rounded to 3
+// significant bits: bf16 queries (8 bits) exactly, weights to 9 bits (bf16 keeps 8), with the range
+// of E5M2 below the largest: a query's elements down to 2^-31 of its row's largest, weights down to
+// 2^-27 of the row's reference. Products of E4M3 and E5M2 codes are exact, sums are fp32. The three
+// terms of Q go into one accumulator, those of W are 3 x 16 columns of one product (V is read
+// once). E is the largest ev so far; a value 2^20 times smaller than the sequence's largest has
+// weights of 7 bits and fewer.
+//
+// Against bf16 operand tiles made from the codes (fa_chunk.cuh): no conversion, which took 2.4 us a
+// tile of 128 keys on one SM, and half the shared-memory traffic. Bound by HBM: 33 KB a tile.
+//
+// Per tile a thread handles one key: x = score - the row's reference m (log2), P = 2^x rounded to 9
+// bits, summed before (log-sum-exp) and after the rounding (divisor of O). The references move only
+// when some x exceeds 4 or some ev exceeds E + 1, which one barrier's vote tells; then the exact
+// maxima are taken and O is rescaled. W <= 2^(4 + 1 + 10), E5M2 ends at 1.75 * 2^15.
+//
+// Warps: 0 loads; 1 issues MMAs; 4-7 softmax and epilogue (and the set-up); 8-11 split the next
+// block's queries, ahead.
+#pragma once
+
+#include "fa_chunk.cuh"
+
+namespace fa {
+
+constexpr int kFewRows = 16, kFewTerms = 3, kFewSlots = 5;
+constexpr int kFewThreads = 384;
+constexpr int kFewD = 128;
+constexpr float kFewGrow = 4.0f;   // log2: how far a score may exceed its row's reference
+constexpr int kFewShift = 10;      // W = P * 2^(ev - E + 10)
+
+struct FewCfg {
+  static constexpr int kSlotBytes = 128 * kFewD + 1024;  // codes, then the scales of each page box at 128 bytes
+  static constexpr int kQBytes = kFewTerms * kFewRows * kFewD, kWBytes = kFewTerms * kFewRows * 128;
+  static constexpr int kOffK = 0, kOffV = kFewSlots * kSlotBytes;
+  static constexpr int kOffQ = 2 * kFewSlots * kSlotBytes;  // two buffers each
+  static constexpr int kOffW = kOffQ + 2 * kQBytes;
+  static constexpr int kOffX = kOffW + 2 * kWBytes;         // maxima and sums: [warp][row], three of them
+  static constexpr int kOffBar = kOffX + 1024;
+  static constexpr int kSmemBytes = kOffBar + 1024 + 1024;
+  static constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 128;  // S: two buffers of 16 columns
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+};
+
+struct FewBars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t full[2][kFewSlots], empty[2][kFewSlots];  // K, V tiles
+  uint64_t s_full[2], s_empty[2], w_full[2], pv_done[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  long long u0, u1, th, first_start;  // (as ChunkBars)
+  int first_h, first_b, first_blk;
+  ChunkSeq first_seq;
+  long long sums[3][4];
+  int many[4];
+  float q_factor[2][kFewRows];  // log2 score per unit of S, before the key's scale
+};
+
+// kind::f8f6f4 with E4M3 A and E5M2 B.
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(uint32_t M, uint32_t N, bool a_mn_major) {
+  return idesc_e4m3_f32(M, N, a_mn_major, false) | (1u << 10);
+}
+
+// x to s significant bits, nearest: c - (c - x) with c = (2^(24 - s) + 1) x.
+template <int kBits>
+__device__ __forceinline__ float2 round_bits2(float2 x) {
+  constexpr float k = (float)(1 << (24 - kBits)) + 1.0f;
+  const float2 c = mul2(x, make_float2(k, k));
+  const float2 e = fma2(x, make_float2(-1.0f, -1.0f), c);
+  return fma2(e, make_float2(-1.0f, -1.0f), c);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
+__device__ __forceinline__ uint32_t pack_e5m2x2(float2 x) {  // x.x in the low byte
+  uint16_t d;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(d) : "f"(x.y), "f"(x.x));
+  return d;
+}
+// x as three E5M2 pairs whose sum is x to 9 bits.
+__device__ __forceinline__ void split_e5m2(float2 x, uint32_t (&t)[kFewTerms]) {
+  const float2 a = round_bits2<3>(x), r = sub2(x, a), b = round_bits2<3>(r);
+  t[0] = pack_e5m2x2(a);
+  t[1] = pack_e5m2x2(b);
+  t[2] = pack_e5m2x2(sub2(r, b));
+}
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// True for all 128 softmax threads when it is for one.
+__device__ __forceinline__ bool few_vote(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float exp2_int(int e) { return e < -126 ? 0.0f : __int_as_float((e + 127) << 23); }
+
+__global__ void __launch_bounds__(kFewThreads, 1)
+    fa_chunk_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
+                        const __nv_bfloat16* __restrict__ q, long long q_stride, const ChunkParams p) {
+  using Cfg = FewCfg;
+  using Walk = ChunkWalk<1>;
+  constexpr int D = kFewD, kPairs = kFewRows / 2;
+  static_assert(sizeof(FewBars) <= 1024, "barrier block");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
+  const uint32_t smem_end = smem_u32(smem_raw) + Cfg::kSmemBytes;  // for the FA_DEBUG bounds checks
+  FewBars* bars = reinterpret_cast<FewBars*>(smem_gen + Cfg::kOffBar);
+  auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
+  const Abort ab{&bars->abort_flag};
+
+  griddep_launch_dependents();
+  if (warp == 2) {
+    if (lane == 0) bars->abort_flag = 0;
+    constexpr int kBars = offsetof(FewBars, mma_done) / 8 + 1;
+    constexpr int kEmptyK = offsetof(FewBars, empty) / 8, kS = offsetof(FewBars, s_full) / 8;
+    const uint32_t first = bar(bars->q_full[0]);
+#pragma unroll
+    for (int j = 0; j < (kBars + 31) / 32; ++j) {
+      const int i = lane + 32 * j;
+      int count = 1;
+      if (i < 2) count = 128;                                  // q_full: the splitting threads
+      else if (i < 4) count = 5;                               // q_empty: the MMAs, the softmax warps
+      else if (i >= kEmptyK && i < kEmptyK + kFewSlots) count = 5;  // K tile: the same (its scales)
+      else if (i >= kS + 2 && i < kS + 6) count = 4;           // s_empty, w_full: the softmax warps
+      if (i < kBars) mbar_init(first + i * 8, count);
+    }
+    fence_barrier_init();
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(&bars->tmem_base), Cfg::kTmemCols);
+    tmem_relinquish();
+    tc_fence_before_sync();
+  } else if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      prefetch_tmap(&tmKs);
+      prefetch_tmap(&tmVs);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // (over the W buffers: nothing is in them yet)
+    chunk_plan<1>(p, bars, reinterpret_cast<int*>(smem_gen + Cfg::kOffW), tid - 128);
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  auto sT = [&](int kv, uint32_t slot) { return smem_base + (kv ? Cfg::kOffV : Cfg::kOffK) + slot * Cfg::kSlotBytes; };
+  const int box_shift = 31 - __clz(p.box_rows);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer (all lanes)
+    // Lane l < 16 loads the codes of page box l of a tile, lane 16 + l its scales; boxes of keys that
+    // no row sees are filled with zeros (page num_pages), as in fa_chunk_kernel.
+    const int groups = 128 / p.box_rows, grp = lane & 15;
+    const bool loads = grp < groups, scales = lane >= 16;
+    const uint32_t box_off = (uint32_t)grp * p.box_rows;
+    uint32_t n = 0;
+    Walk w;
+    for (w.begin(p, bars); w.valid() && !ab.raised(); w.next(p)) {
+      auto place = [&](int v, int& page, int& row) {
+        const int key = w.keys.tile(v) * 128 + (int)box_off, last = key + p.box_rows - 1;
+        page = p.num_pages;
+        row = 0;
+        if (!loads || key > w.keys.vis_hi || (last < w.keys.vis_lo && key >= p.sinks)) return;
+        const int in_seq = p.by_page(key);
+        const long long ti = (long long)w.b * p.max_pages + in_seq;
+        if (!dbg_range(ab, ti, 1, (long long)p.B * p.max_pages)) return;
+        page = __ldg(p.block_table + ti);
+        row = key - in_seq * p.page_size;
+        if (page < 0 || page >= p.num_pages) {
+          atomicOr(&g_fa_error, kErrBadInput);
+          page = p.num_pages;
+        }
+      };
+      int page, row;
+      place(w.v0, page, row);
+      for (int v = w.v0; v < w.v1 && !ab.raised(); ++v, ++n) {
+        const int pg = page, rw = row;
+        if (v + 1 < w.v1) place(v + 1, page, row);  // the next tile's page, read while this one waits
+        const uint32_t slot = n % kFewSlots, phase = (n / kFewSlots) & 1;
+        bool ok = true;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          mbar_wait(bar(bars->empty[kv][slot]), phase ^ 1, ab);
+          const uint32_t to = sT(kv, slot) + box_off * D;
+          if (FA_DEBUG) {
+            ok = !loads || dbg_tma(ab, 0, w.h, rw, pg, D, p.Hkv, p.page_size, p.num_pages + 1, 1, to, p.box_rows * D,
+                                   smem_base, smem_end);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(bars->full[kv][slot]), 128 * D + 128);
+          __syncwarp();
+          if (loads && !scales)
+            tma_load_4d(to, kv ? &tmV : &tmK, bar(bars->full[kv][slot]), 0, w.h, rw, pg);
+          else if (loads)
+            tma_load_2d(sT(kv, slot) + 128 * D + grp * 128, kv ? &tmVs : &tmKs, bar(bars->full[kv][slot]), rw,
+                        pg * p.Hkv + w.h);
+        }
+        if (!ok) break;
+      }
+    }
+    for (uint32_t i = n > kFewSlots ? n - kFewSlots : 0; i < n; ++i)  // every load issued lands before the CTA exits
+      for (int kv = 0; kv < 2; ++kv) mbar_drain(bar(bars->full[kv][i % kFewSlots]), (i / kFewSlots) & 1);
+  } else if (warp == 3) {
+    if (blockIdx.x == 0)
+      report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, lane, 32);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (elect_one()) {
+      constexpr uint32_t idS = idesc_e4m3_e5m2(128, kFewRows, false);            // K: rows of 128 bytes
+      constexpr uint32_t idO = idesc_e4m3_e5m2(D, kFewTerms * kFewRows, true);   // V^T: columns are contiguous
+      uint32_t n = 0, blocks = 0;
+      auto issue_s = [&](uint32_t i, uint32_t qb, bool last) {
+        const uint32_t slot = i % kFewSlots, buf = i & 1;
+        mbar_wait(bar(bars->full[0][slot]), (i / kFewSlots) & 1, ab);
+        mbar_wait(bar(bars->s_empty[buf]), ((i >> 1) & 1) ^ 1, ab);
+        tc_fence_after_sync();
+        const uint32_t k_smem = sT(0, slot), q_smem = smem_base + Cfg::kOffQ + qb * Cfg::kQBytes;
+#pragma unroll
+        for (int term = 0; term < kFewTerms; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_ss_f8(tmem + Cfg::kColS + buf * kFewRows, sdesc_kmajor(k_smem + kk * 32),
+                      sdesc_kmajor(q_smem + term * (kFewRows * D) + kk * 32), idS, term > 0 || kk > 0);
+        mma_commit(bar(bars->s_full[buf]));
+        mma_commit(bar(bars->empty[0][slot]));
+        if (last) mma_commit(bar(bars->q_empty[qb]));
+      };
+      Walk w;
+      for (w.begin(p, bars); w.valid(); w.next(p), ++blocks) {
+        const int nv = w.v1 - w.v0;
+        const uint32_t qb = blocks & 1;
+        mbar_wait(bar(bars->q_full[qb]), (blocks >> 1) & 1, ab);
+        tc_fence_after_sync();
+        issue_s(n, qb, nv == 1);
+        for (int v = 0; v < nv; ++v, ++n) {
+          if (v + 1 < nv) issue_s(n + 1, qb, v + 2 == nv);
+          const uint32_t slot = n % kFewSlots, buf = n & 1;
+          mbar_wait(bar(bars->full[1][slot]), (n / kFewSlots) & 1, ab);
+          mbar_wait(bar(bars->w_full[buf]), (n >> 1) & 1, ab);
+          tc_fence_after_sync();
+          const uint32_t w_smem = smem_base + Cfg::kOffW + buf * Cfg::kWBytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss_f8(tmem + Cfg::kColO, sdesc_mnmajor(sT(1, slot) + kk * 4096, 16384), sdesc_kmajor(w_smem + kk * 32),
+                      idO, v > 0 || kk > 0);
+          mma_commit(bar(bars->pv_done[buf]));
+          mma_commit(bar(bars->empty[1][slot]));
+        }
+      }
+      mma_commit(bar(bars->mma_done));
+      mbar_drain(bar(bars->mma_done), 0);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------------------- softmax + epilogue: a key, then a column of O
+    const int key_in = tid - 128, wq = warp - 4;
+    const uint32_t lane_field = (uint32_t)(wq * 32) << 16;
+    const uint32_t scale_at = 128 * D + ((key_in >> box_shift) << 7) + (key_in & (p.box_rows - 1));
+    float* sX = reinterpret_cast<float*>(smem_gen + Cfg::kOffX);  // [3][warp][row]
+    int* sE = reinterpret_cast<int*>(smem_gen + Cfg::kOffX + 768);  // [warp]
+    const uint32_t w_at = (uint32_t)key_in;  // byte of this key in a row of W, before the swizzle
+    uint32_t n = 0, blocks = 0;
+    int4 split = make_int4(0, 0, 0, 0);  // the block that this piece hands on to the next one
+    auto pv_wait = [&](uint32_t i) {     // W V of tile i has been added
+      mbar_wait(bar(bars->pv_done[i & 1]), (i >> 1) & 1, ab);
+      tc_fence_after_sync();
+    };
+    Walk w;
+    for (w.begin(p, bars); w.valid(); w.next(p), ++blocks) {
+      const int nv = w.v1 - w.v0, rows = w.ntok * p.G, pairs = (rows + 1) >> 1;
+      const int pos0 = w.pos0(p.tq, 0), pos1 = pos0 + w.ntok - 1;
+      const uint32_t qb = blocks & 1;
+      float2 c2[kPairs], m2[kPairs], l2[kPairs], lr2[kPairs];
+      mbar_wait(bar(bars->q_full[qb]), (blocks >> 1) & 1, ab);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        c2[i] = *reinterpret_cast<const float2*>(&bars->q_factor[qb][2 * i]);
+        m2[i] = make_float2(0.0f, 0.0f);
+        l2[i] = lr2[i] = make_float2(0.0f, 0.0f);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars->q_empty[qb]));
+      int E = -1000;
+      uint32_t unset = (1u << rows) - 1u;  // rows that have seen no key: their reference is not one yet
+
+      for (int v = 0; v < nv; ++v, ++n) {
+        const uint32_t slot = n % kFewSlots, buf = n & 1;
+        const int key0 = w.keys.tile(w.v0 + v) * 128, key = key0 + key_in;
+        mbar_wait(bar(bars->full[0][slot]), (n / kFewSlots) & 1, ab);
+        const uint32_t ks = smem_gen[sT(0, slot) - smem_base + scale_at];
+        mbar_wait(bar(bars->s_full[buf]), (n >> 1) & 1, ab);
+        tc_fence_after_sync();
+        float2 a[kPairs];
+        {
+          uint32_t r0[8], r1[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+          tmem_ld8(tmem + lane_field + Cfg::kColS + buf * kFewRows, r0);
+          if (pairs > 4) tmem_ld8(tmem + lane_field + Cfg::kColS + buf * kFewRows + 8, r1);
+          tmem_wait_ld(r0);
+          tmem_wait_ld(r1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = make_float2(__uint_as_float(r0[2 * i]), __uint_as_float(r0[2 * i + 1]));
+            a[i + 4] = make_float2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1]));
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(bars->s_empty[buf]));
+          mbar_arrive(bar(bars->empty[0][slot]));
+        }
+        mbar_wait(bar(bars->full[1][slot]), (n / kFewSlots) & 1, ab);
+        const uint32_t vs = smem_gen[sT(1, slot) - smem_base + scale_at];
+        const float kf = ks == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float((int)max(ks, 1u) << 23);
+
+        // scores against the references, -inf where masked; is the key seen at all?
+        const bool all = pos0 >= 0 && key0 + 127 < w.s.n &&
+                         (p.win_r < 0 || key0 + 127 <= (long long)pos0 + p.win_r) &&
+                         (p.win_l < 0 || key0 >= pos1 - p.win_l || key0 + 127 < p.sinks);
+        bool seen = true;
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          if (i >= pairs) break;
+          a[i] = fma2(mul2(a[i], c2[i]), make_float2(kf, kf), make_float2(-m2[i].x, -m2[i].y));
+        }
+        if (!all) {
+          seen = false;
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            if (i >= pairs) break;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int pos = pos0 + p.by_group(2 * i + e);
+              const bool vis = pos >= 0 && key < w.s.n && (p.win_r < 0 || key <= (long long)pos + p.win_r) &&
+                               (p.win_l < 0 || key >= pos - p.win_l || key < p.sinks) && 2 * i + e < rows;
+              seen |= vis;
+              if (!vis) (e ? a[i].y : a[i].x) = -INFINITY;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          if (i >= pairs) break;
+          most = max3(most, a[i].x, a[i].y);
+        }
+        const int ev = seen && vs != (uint32_t)kScaleNan ? (int)vs - 127 : -1000;
+        if (few_vote(most > kFewGrow || ev > E + 1 || unset != 0)) {
+          // exact maxima over the tile's keys; the sums and O follow the new references
+          int em = __reduce_max_sync(0xffffffffu, ev);
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            if (i >= pairs) break;
+            const float x = warp_max_f32(a[i].x), y = warp_max_f32(a[i].y);
+            if (lane == 0) *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * i]) = make_float2(x, y);
+          }
+          if (lane == 0) sE[wq] = em;
+          named_bar_sync(2, 128);
+          em = max(max(sE[0], sE[1]), max(sE[2], sE[3]));
+          const int e_new = max(E, em);
+          const float e_step = E <= -1000 ? 0.0f : exp2_int(E - e_new);
+          float2 alpha[kPairs];
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            alpha[i] = make_float2(1.0f, 1.0f);
+            if (i >= pairs) continue;
+            float2 x = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float2 y = *reinterpret_cast<const float2*>(&sX[u * kFewRows + 2 * i]);
+              x = make_float2(fmaxf(x.x, y.x), fmaxf(x.y, y.y));
+            }
+            float2 up;  // rise of the references; a first one may lie anywhere
+            auto rise = [&](float most_r, int r, float& up_r, float& alpha_r) {
+              const bool first = (unset >> r) & 1;
+              up_r = first ? (most_r == -INFINITY ? 0.0f : most_r) : fmaxf(most_r, 0.0f);
+              alpha_r = first ? 1.0f : ex2_approx(-up_r);
+              if (most_r != -INFINITY) unset &= ~(1u << r);
+            };
+            rise(x.x, 2 * i, up.x, alpha[i].x);
+            rise(x.y, 2 * i + 1, up.y, alpha[i].y);
+            m2[i] = add2(m2[i], up);
+            a[i] = sub2(a[i], up);
+            l2[i] = mul2(l2[i], alpha[i]);
+            lr2[i] = mul2(lr2[i], alpha[i]);
+          }
+          E = e_new;
+          if (v > 0) {
+            pv_wait(n - 1);
+#pragma unroll
+            for (int term = 0; term < kFewTerms; ++term)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                if (hf * 4 >= pairs) continue;
+                uint32_t o[8];
+                const uint32_t at = tmem + lane_field + Cfg::kColO + term * kFewRows + hf * 8;
+                tmem_ld8(at, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) * (alpha[hf * 4 + i].x * e_step));
+                  o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) * (alpha[hf * 4 + i].y * e_step));
+                }
+                tmem_st8(at, o);
+              }
+            tmem_wait_st();
+          }
+          named_bar_sync(2, 128);  // sX and sE have been read
+        }
+        const float vf = vs == (uint32_t)kScaleNan && seen ? __int_as_float(0x7fc00000)
+                         : seen                          ? exp2_int((int)vs - 127 - E + kFewShift)
+                                                         : 0.0f;
+        if (n >= 2) mbar_wait(bar(bars->pv_done[buf]), ((n >> 1) & 1) ^ 1, ab);  // tile n - 2 has read this W buffer
+        const uint32_t w_smem = smem_base + Cfg::kOffW + buf * Cfg::kWBytes;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          if (i >= pairs) break;
+          const float2 pe = make_float2(ex2_approx(a[i].x), ex2_approx(a[i].y));
+          l2[i] = add2(l2[i], pe);
+          const float2 pr = round_bits2<9>(pe);
+          lr2[i] = add2(lr2[i], pr);
+          uint32_t t[kFewTerms];
+          split_e5m2(mul2(pr, make_float2(vf, vf)), t);
+#pragma unroll
+          for (int term = 0; term < kFewTerms; ++term) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = term * kFewRows + 2 * i + e;
+              st_shared_u8(w_smem + r * 128 + (w_at ^ ((r & 7) << 4)), e ? t[term] >> 8 : t[term]);
+            }
+          }
+        }
+        if (!seen) {  // the row of a key that no row sees may hold anything: 0 (its weights are 0)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) st_shared_v4(sT(1, slot) + key_in * D + i * 16, 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars->w_full[buf]));
+      }
+
+      // ---- epilogue: this thread's column of every row
+      const bool whole = w.whole();
+      const int slot = 2 * (int)blockIdx.x + (w.start > w.u0 ? 1 : 0);  // of its partial
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        if (i >= pairs) break;
+        float2 a = l2[i], b = lr2[i];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+          a = add2(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, off), __shfl_xor_sync(0xffffffffu, a.y, off)));
+          b = add2(b, make_float2(__shfl_xor_sync(0xffffffffu, b.x, off), __shfl_xor_sync(0xffffffffu, b.y, off)));
+        }
+        if (lane == 0) {
+          *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * i]) = a;
+          *reinterpret_cast<float2*>(&sX[(4 + wq) * kFewRows + 2 * i]) = b;
+        }
+      }
+      named_bar_sync(2, 128);
+      if (nv > 0) pv_wait(n - 1);
+      const float e_unit = exp2_int(max(E, -110) - kFewShift);
+      const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.pieces * 128;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (hf * 8 >= rows) break;
+        float o[8];
+#pragma unroll
+        for (int term = 0; term < kFewTerms; ++term) {
+          uint32_t r[8];
+          tmem_ld8(tmem + lane_field + Cfg::kColO + term * kFewRows + hf * 8, r);
+          tmem_wait_ld(r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = term == 0 ? __uint_as_float(r[i]) : o[i] + __uint_as_float(r[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = hf * 8 + i;
+          if (r >= rows) break;
+          float l = 0.0f, lr = 0.0f;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            l += sX[u * kFewRows + r];
+            lr += sX[(4 + u) * kFewRows + r];
+          }
+          const bool dead = !(lr > 0.0f) && lr == lr;  // no visible key (a NaN sum is not one)
+          const float value = dead ? 0.0f : o[i] * e_unit / lr;
+          const float m = (i & 1) ? m2[r >> 1].y : m2[r >> 1].x;
+          const float lse2 = l > 0.0f ? m + lg2_approx(l) : (l == l ? -INFINITY : l);
+          const int itok = p.by_group(r), head = w.h * p.G + r - itok * p.G;
+          const long long tok = (long long)w.s.c0 + w.i0 + itok;
+          if (whole) {
+            const long long oi = (tok * p.Hq + head) * D + key_in, li = (long long)head * p.total + tok;
+            if (dbg_range(ab, oi, 1, o_size)) p.o[oi] = __float2bfloat16_rn(value);
+            if (key_in == 0 && dbg_range(ab, li, 1, (long long)p.Hq * p.total))
+              p.lse[li] = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
+          } else {
+            const long long pi = (long long)slot * 128;
+            if (dbg_range(ab, pi + r, 1, part_rows)) {
+              p.o_part[pi * D + ((key_in >> 2) * 128 + r) * 4 + (key_in & 3)] = value;
+              if (key_in == 0) p.lse_part[pi + r] = lse2;
+            }
+          }
+        }
+      }
+      tc_fence_before_sync();
+      named_bar_sync(2, 128);  // the sums have been read
+      if (!whole && w.start >= w.u0) {
+        const long long T = bars->th * p.Hkv;
+        const int last = ChunkSplit(T, (int)min((long long)p.pieces, T)).of(w.start + w.keys.cnt - 1);
+        split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * last + (slot & 1));
+      }
+    }
+    if (key_in == 0 && dbg_range(ab, blockIdx.x, 1, p.pieces)) p.split[blockIdx.x] = split;
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------- queries: eight threads a row, 16 elements each
+    const int ct = tid - 256, row = ct >> 3, c = ct & 7;
+    uint32_t blocks = 0;
+    Walk w;
+    for (w.begin(p, bars); w.valid(); w.next(p), ++blocks) {
+      const uint32_t qb = blocks & 1;
+      const int itok = p.by_group(row), head = w.h * p.G + row - itok * p.G;
+      const long long qi = ((long long)w.s.c0 + w.i0 + itok) * q_stride + (long long)head * D + c * 16;
+      uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (row < w.ntok * p.G) {
+        x[0] = __ldg(reinterpret_cast<const uint4*>(q + qi));
+        x[1] = __ldg(reinterpret_cast<const uint4*>(q + qi + 8));
+      }
+      const uint32_t in[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = __vmaxu2(most, in[i] & 0x7fff7fffu);
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, off));
+      // the row's largest magnitude goes to [2^14, 2^15); an infinity or a NaN stays one (as NaN)
+      const int top = (int)(max(most & 0xffffu, most >> 16) >> 7);
+      const int up = min(14 + 127 - top, 126);
+      const float f = top == 255 ? __int_as_float(0x7fc00000) : exp2_int(up);
+      mbar_wait(bar(bars->q_empty[qb]), ((blocks >> 1) & 1) ^ 1, ab);
+      uint32_t out[kFewTerms][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t t[kFewTerms];
+        split_e5m2(mul2(make_float2(bf16lo_to_f32(in[i]), bf16hi_to_f32(in[i])), make_float2(f, f)), t);
+#pragma unroll
+        for (int term = 0; term < kFewTerms; ++term)
+          out[term][i >> 1] = (i & 1) ? out[term][i >> 1] | t[term] << 16 : t[term];
+      }
+      const uint32_t to = smem_base + Cfg::kOffQ + qb * Cfg::kQBytes + row * D + ((c ^ (row & 7)) << 4);
+#pragma unroll
+      for (int term = 0; term < kFewTerms; ++term)
+        st_shared_v4(to + term * (kFewRows * D), out[term][0], out[term][1], out[term][2], out[term][3]);
+      if (c == 0) bars->q_factor[qb][row] = p.scale_log2 * exp2_int(-up);
+      fence_proxy_async_smem();
+      mbar_arrive(bar(bars->q_full[qb]));
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+}  // namespace fa

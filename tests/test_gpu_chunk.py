@@ -71,6 +71,43 @@ def test_many_sequences():
     check(Batch(new, keys, 4, 2, 128, 32, True, seed=2), "sinks")
 
 
+@pytest.mark.parametrize("mask", list(MASKS))
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (4, 2), (6, 2), (8, 2), (5, 1), (7, 1), (16, 2), (16, 1)])
+def test_few_rows_over_quantised_pages(mask, Hq, Hkv):
+    """Blocks of up to 16 rows (tokens times heads), d = 128: steps, short speculative chunks, empty sequences."""
+    most = max(1, 16 // (Hq // Hkv))
+    check(Batch([1] * 5, [1, 130, 128, 777, 2000], Hq, Hkv, 128, 16, True, seed=Hq), mask)
+    check(Batch([most, 0, 1, most], [most, 9, 300, 1500], Hq, Hkv, 128, 48, True, seed=Hq + 1, pad=2), mask)
+
+
+def test_few_rows_cut_from_a_longer_chunk():
+    check(Batch([50] + [0] * 3 + [1] * 20, [700] + [40] * 23, 4, 1, 128, 64, True, seed=3))
+    check(Batch([60] + [1] * 59, [333] + [2] * 59, 8, 1, 128, 64, True, seed=4), "far")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.7, 1e-4, 30.0])
+def test_few_rows_scales_and_dominant_keys(scale):
+    b = Batch([4, 1], [400, 3000], 4, 2, 128, 16, True, seed=13)
+    check(b, "causal", scale)
+    b.q[:] = b.q * 30
+    check(b, "sinks", scale if scale < 1 else 0.1)
+
+
+def test_few_rows_references_move():
+    """Scores and value scales that grow, fall and jump from tile to tile; queries of very different size."""
+    b = Batch([3], [2000], 2, 1, 128, 16, False, seed=14, spare=0)
+    rows = [(b.table[0, j // 16], j % 16) for j in range(2000)]
+    for j, at in enumerate(rows):
+        b.k[at] = (b.k[at].float() * (0.2 + j / 400)).bfloat16()
+        b.v[at] = (b.v[at].float() * 2.0 ** ((j // 128) % 5 * 3 - 6)).bfloat16()
+    b.q[0] = b.q[0] * 2.0 ** -20
+    b.q[1, 0, 5:] = b.q[1, 0, 5:] * 2.0 ** -18
+    from chunk_cases import quantise
+    (b.k, b.ks), (b.v, b.vs), b.f8 = quantise(b.k), quantise(b.v), True
+    check(b)
+    check(b, "sinks")
+
+
 @pytest.mark.parametrize("f8", [False, True])
 def test_rows_without_a_key_or_a_place(f8):
     # more new rows than positions, an empty sequence with new rows, an empty cache

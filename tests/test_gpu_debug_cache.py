@@ -36,6 +36,9 @@ def use_debug_lib(debug_lib, monkeypatch):
     ([9, 3], [4, 0], 4, 2, 128, 16, (-1, -1), 0),
     ([1, 1, 1], [9000, 20000, 1], 16, 1, 64, 128, (-1, -1), 0),
     ([2], [30000], 128, 1, 128, 80, (-1, -1), 0),
+    ([1, 1, 1], [9000, 20000, 1], 16, 1, 128, 128, (-1, -1), 0),
+    ([4, 2, 0, 4], [500, 2, 7, 1100], 4, 1, 128, 48, (40, -1), 6),
+    ([1, 3, 1], [700, 3000, 130], 5, 1, 128, 16, (200, -1), 130),
 ])
 def test_write_attend_read(new, keys, Hq, Hkv, d, page, window, sinks, f8):
     b = Batch(new, keys, Hq, Hkv, d, page, f8, pad=5, seed=sum(keys))

@@ -707,7 +707,7 @@ template <int D, int kTiles>
 int chunk_merge_launch(int pieces, const fa::ChunkParams& p, cudaStream_t stream) {
   const long long rows = std::min<long long>((long long)p.total * p.G, kTiles * 128);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pieces, (unsigned)((rows + fa::merge_rows(kTiles) - 1) / fa::merge_rows(kTiles)));
+  cfg.gridDim = dim3(pieces, (unsigned)((rows + fa::kMergeRows - 1) / fa::kMergeRows));
   cfg.blockDim = dim3(fa::kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1105,7 +1105,7 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   const double blocks = (double)(total / ((few ? 1 : tiles) * tq)) + std::min(B, total);
   const int key_tiles = (max_keys + 127) / 128;
   const double most = blocks * Hkv * key_tiles;
-  const int pieces = most < sms ? (int)most : std::min(sms, fa::kMergeMaxPieces);
+  const int pieces = most < sms ? (int)most : sms;
   int box_rows = 16;
   while (box_rows < 128 && page_size % (2 * box_rows) == 0) box_rows *= 2;
   CUtensorMap m[5];

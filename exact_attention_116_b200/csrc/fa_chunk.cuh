@@ -74,6 +74,7 @@ struct ChunkCfg {
   static constexpr int kConvThreads = kF8 ? 256 : 0;
   static constexpr int kConvWarps = kConvThreads / 32;
   static constexpr int kThreads = 128 + kSoftThreads + kConvThreads;
+  static constexpr int kBlockReaders = 2 + kSoftWarps + kConvThreads / 32;  // the loads', the MMAs', ...
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;  // a thread's at launch
   static constexpr int kLoadRegs = 56, kConvRegs = kTiles == 2 ? 48 : 64;
   static constexpr int kSoftRegs = kTiles == 2 ? (kF8 ? 88 : 104) : kF8 ? 128 : 0;  // 0: as launched
@@ -90,7 +91,7 @@ struct ChunkCfg {
   static constexpr int kOffX = kOffRaw + kRawSlots * kRawSlotBytes;
   static constexpr int kXBytes = 4096 * kTiles;       // per tile: maxima [parity][half][row], sums [sum][half][row]
   static constexpr int kOffBar = kOffX + kXBytes;
-  static constexpr int kSmemBytes = kOffBar + 1024 + 1024;  // barriers + alignment slack
+  static constexpr int kSmemBytes = kOffBar + 1536 + 1024;  // barriers + alignment slack
   static constexpr bool kShareS = kTiles == 2 && D == 128;  // one S buffer for both tiles
   static constexpr uint32_t kColS0 = 0, kColS1 = kShareS ? 0 : 128;
   static constexpr uint32_t kColP0 = kShareS ? 128 : 384, kColP1 = kShareS ? 192 : 448;
@@ -112,23 +113,6 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b) {
   s.n = (n < 0 || n > (long long)p.max_pages * p.page_size) ? 0 : n;
   return s;
 }
-
-template <class Cfg>
-struct ChunkBars {
-  uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[Cfg::kSlots], kv_empty[Cfg::kSlots];
-  uint64_t raw_full[Cfg::kRawSlots + 1], raw_empty[Cfg::kRawSlots + 1];
-  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t mma_done;
-  uint32_t tmem_base;
-  int abort_flag;
-  long long u0, u1, th;     // the piece, the length of one head's list
-  long long first_start;    // the piece's first block: its position on the list of all heads
-  int first_h, first_b, first_blk;
-  ChunkSeq first_seq;
-  long long sums[3][4];     // scans
-  int many[4];
-};
 
 // Keys visible to some row of a block, and the tiles that hold them: tile v of the block is key
 // tile v for v < ns (sinks left of the window), lo + v - ns from there on; cnt >= 1 in all (a
@@ -155,9 +139,37 @@ __device__ __forceinline__ ChunkKeys chunk_keys(const ChunkParams& p, int n, int
   return k;
 }
 
-// A walk over the blocks of one piece. A block: head h, sequence b, tokens [i0, i0 + ntok) of its
-// chunk; its tiles [v0, v1) belong to the piece. It lies in the piece as a whole (whole()), or is
-// spread over several.
+// A block as its roles need it: head h, sequence b of n keys, ntok tokens from packed row c0 on, the
+// first at position pos0; key tiles [v0, v1) of it belong to this CTA's piece.
+struct ChunkBlock {
+  int h, b, n, c0, ntok, pos0;
+  ChunkKeys keys;
+  int v0, v1;  // v1 = 0: the end of the list
+  int slot;    // of its partial result; -1: the block lies in the piece as a whole
+};
+// One thread walks over the piece's blocks and hands them to the other roles through a ring.
+constexpr int kBlockRing = 4;
+
+template <class Cfg>
+struct ChunkBars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[Cfg::kSlots], kv_empty[Cfg::kSlots];
+  uint64_t raw_full[Cfg::kRawSlots + 1], raw_empty[Cfg::kRawSlots + 1];
+  uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t block_full[kBlockRing], block_empty[kBlockRing];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  long long u0, u1, th;     // the piece, the length of one head's list
+  long long first_start;    // the piece's first block: its position on the list of all heads
+  int first_h, first_b, first_blk;
+  ChunkSeq first_seq;
+  long long sums[3][4];     // scans
+  int many[4];
+  ChunkBlock block[kBlockRing];
+};
+
+// A walk over the blocks of one piece: block blk of sequence b for head h.
 template <int kTiles>
 struct ChunkWalk {
   long long u0, u1;  // the piece's range of the list of all heads
@@ -165,7 +177,7 @@ struct ChunkWalk {
   ChunkSeq s;
   ChunkKeys keys;
   long long start;  // position of the block's first tile on the list of all heads
-  int i0, ntok, v0, v1;
+  int i0, ntok;
 
   __device__ __forceinline__ void set(const ChunkParams& p) {
     const int tokens = kTiles * p.tq;
@@ -173,8 +185,6 @@ struct ChunkWalk {
     ntok = min(tokens, s.rows - i0);
     const int pos0 = s.n - s.rows + i0;
     keys = chunk_keys(p, s.n, pos0, pos0 + ntok - 1);
-    v0 = (int)max(0LL, u0 - start);
-    v1 = (int)min((long long)keys.cnt, u1 - start);
   }
   __device__ __forceinline__ bool valid() const { return start < u1; }
   __device__ __forceinline__ bool whole() const { return start >= u0 && start + keys.cnt <= u1; }
@@ -205,7 +215,10 @@ struct ChunkWalk {
     }
     set(p);
   }
-  __device__ __forceinline__ int pos0(int tq, int t) const { return s.n - s.rows + i0 + t * tq; }
+  __device__ __forceinline__ ChunkBlock block() const {
+    return {h, b, s.n, s.c0 + i0, ntok, s.n - s.rows + i0, keys, (int)max(0LL, u0 - start),
+            (int)min((long long)keys.cnt, u1 - start), whole() ? -1 : 2 * (int)blockIdx.x + (start > u0 ? 1 : 0)};
+  }
 };
 
 // The list of all heads, T tiles, in pieces: the first T % pieces of them one tile longer.
@@ -225,6 +238,53 @@ struct ChunkSplit {
     return u < head ? (int)(u / (each + 1)) : (int)(more + (u - head) / each);
   }
 };
+
+// Publishes the piece's blocks, and the block that the piece hands on to the next one (for the merge).
+template <int kTiles, class Bars>
+__device__ __forceinline__ void chunk_publish(const ChunkParams& p, Bars* bars, Abort ab) {
+  ChunkWalk<kTiles> w;
+  int4 split = make_int4(0, 0, 0, 0);
+  uint32_t i = 0;
+  auto put = [&](const ChunkBlock& b) {
+    const uint32_t slot = i % kBlockRing;
+    mbar_wait(smem_u32(&bars->block_empty[slot]), ((i / kBlockRing) & 1) ^ 1, ab);
+    bars->block[slot] = b;
+    mbar_arrive(smem_u32(&bars->block_full[slot]));
+    ++i;
+  };
+  for (w.begin(p, bars); w.valid() && !ab.raised(); w.next(p)) {
+    put(w.block());
+    if (!w.whole() && w.start >= w.u0) {
+      const long long T = bars->th * p.Hkv;
+      const int last = ChunkSplit(T, (int)min((long long)p.pieces, T)).of(w.start + w.keys.cnt - 1);
+      split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * last + (w.start > w.u0 ? 1 : 0));
+    }
+  }
+  if (!ab.raised()) put(ChunkBlock{});
+  if (dbg_range(ab, blockIdx.x, 1, p.pieces)) p.split[blockIdx.x] = split;
+}
+// Block i of the piece (all lanes of a warp, or one thread); null: there is none, or the CTA gave up.
+template <class Bars>
+__device__ __forceinline__ const ChunkBlock* chunk_take(Bars* bars, uint32_t i, Abort ab) {
+  const uint32_t slot = i % kBlockRing;
+  const bool ok = mbar_wait(smem_u32(&bars->block_full[slot]), (i / kBlockRing) & 1, ab);
+  return ok && bars->block[slot].v1 > 0 ? &bars->block[slot] : nullptr;
+}
+template <class Bars>
+__device__ __forceinline__ void chunk_release(Bars* bars, uint32_t i) {
+  mbar_arrive(smem_u32(&bars->block_empty[i % kBlockRing]));
+}
+// True for all `threads` threads at the barrier when it is for each of them.
+__device__ __forceinline__ bool all_agree(bool x, uint32_t id, uint32_t threads) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
 
 // The set-up of one CTA by 128 threads (tid 0..127 here): which piece is its own, and where the
 // piece's first block lies. Blocks are counted per run of sequences, then key tiles per run of
@@ -365,21 +425,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// Row maximum of kC scores with the window and the sinks masked: key kbase + cc is visible when
-// it lies in [kmin, kmax] or is one of the first `sinks` keys and at most kmax.
-template <int kC>
-__device__ __forceinline__ void chunk_mask(float (&x)[kC], int kbase, int kmin, int kmax, int sinks) {
-  const bool any = kmax >= kmin;
-  const unsigned span = any ? (unsigned)(kmax - kmin) : 0u;
-  const int off = any ? kbase - kmin : -(1 << 30);
-  if (kbase < sinks) {
-    const int lim = min(sinks - 1, kmax) - kbase;
+// Which of 64 keys from kbase on a row sees: those in [kmin, kmax] and the first `sinks` up to kmax.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+__device__ __forceinline__ void chunk_visible(int kbase, int kmin, int kmax, int sinks, uint32_t (&m)[2]) {
+  const int from = kmin - kbase, end = kmax + 1 - kbase, first = min(sinks, kmax + 1) - kbase;
 #pragma unroll
-    for (int cc = 0; cc < kC; ++cc) x[cc] = ((unsigned)(off + cc) <= span || cc <= lim) ? x[cc] : -INFINITY;
-  } else {
-#pragma unroll
-    for (int cc = 0; cc < kC; ++cc) x[cc] = ((unsigned)(off + cc) <= span) ? x[cc] : -INFINITY;
-  }
+  for (int w = 0; w < 2; ++w)
+    m[w] = (bits_below(end - 32 * w) & ~bits_below(from - 32 * w)) | bits_below(first - 32 * w);
 }
 
 // 2^x of a pair on the FMA pipe, as exp2_poly2 with a degree-5 polynomial (relative error 6e-8 of
@@ -426,8 +478,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
                     const __grid_constant__ CUtensorMap tmVs, const ChunkParams p) {
   using Cfg = ChunkCfg<D, kF8, kTiles>;
   using Bars = ChunkBars<Cfg>;
-  using Walk = ChunkWalk<kTiles>;
-  static_assert(sizeof(Bars) <= 1024, "barrier block");
+  static_assert(sizeof(Bars) <= 1536, "barrier block");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
@@ -452,6 +503,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       if (kF8 && i >= kKv && i < kKv + Cfg::kSlots) count = Cfg::kConvWarps;               // kv_full: converting warps
       if (kF8 && i >= kRaw + Cfg::kRawSlots + 1 && i < kS) count = Cfg::kConvWarps;         // raw_empty
       if (i >= kS + 2 && i < kS + 6) count = 256;                                           // s_empty, p_full
+      if (i >= kBars - 1 - kBlockRing && i < kBars - 1) count = Cfg::kBlockReaders;         // block_empty
       if (i < kBars) mbar_init(first + i * 8, count);
     }
     fence_barrier_init();
@@ -475,7 +527,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   const uint32_t sKV = smem_base + Cfg::kOffKV, sRaw = smem_base + Cfg::kOffRaw;
   auto sQ = [&](int t) { return smem_base + Cfg::kOffQ + t * Cfg::kTileBytes; };
-  auto begin = [&](Walk& w) { w.begin(p, bars); };
 
   // Registers: the launch gives each thread the same number (Cfg::kRegs); the producer and MMA warps
   // and the converting ones hand some back, and the softmax warps take them. The sum stays within
@@ -493,16 +544,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     const uint32_t box_off = (uint32_t)grp * p.box_rows;
     uint32_t n = 0, qn[2] = {0, 0};  // K/V tiles issued, Q tiles issued
     constexpr int kRing = kF8 ? Cfg::kRawSlots : Cfg::kSlots;
-    Walk w;
-    begin(w);
     // page and row of this lane's box of tile v of block w; page num_pages: zeros
-    auto place = [&](const Walk& x, int v, int& page, int& row) {
-      const int key = x.keys.tile(v) * 128 + (int)box_off, last = key + p.box_rows - 1;
+    auto place = [&](const ChunkBlock& w, int v, int& page, int& row) {
+      const int key = w.keys.tile(v) * 128 + (int)box_off, last = key + p.box_rows - 1;
       page = p.num_pages;
       row = 0;
-      if (!loads || key > x.keys.vis_hi || (last < x.keys.vis_lo && key >= p.sinks)) return;
+      if (!loads || key > w.keys.vis_hi || (last < w.keys.vis_lo && key >= p.sinks)) return;
       const int in_seq = p.by_page(key);
-      const long long ti = (long long)x.b * p.max_pages + in_seq;
+      const long long ti = (long long)w.b * p.max_pages + in_seq;
       if (!dbg_range(ab, ti, 1, (long long)p.B * p.max_pages)) return;
       page = __ldg(p.block_table + ti);
       row = key - in_seq * p.page_size;
@@ -512,12 +561,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       }
     };
     int page = 0, row = 0;
-    for (; w.valid() && !ab.raised();) {
+    const ChunkBlock* block;
+    for (uint32_t i = 0; (block = chunk_take(bars, i, ab)) && !ab.raised(); ++i) {
+      const ChunkBlock& w = *block;
       const int nact = (kTiles == 2 && w.ntok > p.tq) ? 2 : 1;
       if (lane == 0) {
         for (int t = 0; t < nact; ++t) {
           mbar_wait(bar(bars->q_empty[t]), (qn[t] & 1) ^ 1, ab);
-          const int tok = w.s.c0 + w.i0 + t * p.tq;
+          const int tok = w.c0 + t * p.tq;
           bool ok = true;
           for (int bx = 0; bx < Cfg::kBoxes; ++bx)
             ok = ok && dbg_tma(ab, bx * 64, 0, w.h, tok, D, p.G, p.Hkv, p.total, 2, sQ(t) + bx * 16384, 16384,
@@ -564,7 +615,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
           }
         }
       }
-      w.next(p);
+      __syncwarp();
+      if (lane == 0) chunk_release(bars, i);
     }
     // every load issued lands before the CTA exits
     for (uint32_t i = n > kRing ? n - kRing : 0; i < n; ++i)
@@ -573,6 +625,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       for (int t = 0; t < 2; ++t)
         if (qn[t] > 0) mbar_drain(bar(bars->q_full[t]), (qn[t] - 1) & 1);
   } else if (warp == 3) {
+    if (lane == 0) chunk_publish<kTiles>(p, bars, ab);
+  } else if (warp == 2) {
     if (blockIdx.x == 0) report_bad_batch(p.cu, p.seqlens, p.B, p.total, max_keys, lane, 32);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
@@ -613,8 +667,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
                  !first || kk > 0);
         mma_commit(bar(bars->pv_done[t]));
       };
-      Walk w;
-      for (begin(w); w.valid(); w.next(p)) {
+      const ChunkBlock* block;
+      for (uint32_t i = 0; (block = chunk_take(bars, i, ab)); ++i) {
+        const ChunkBlock& w = *block;
         const int nact = (kTiles == 2 && w.ntok > p.tq) ? 2 : 1, nv = w.v1 - w.v0;
         for (int t = 0; t < nact; ++t) mbar_wait(bar(bars->q_full[t]), (qn[t]++) & 1, ab);
         tc_fence_after_sync();
@@ -633,6 +688,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
           }
           mma_commit(bar(bars->kv_empty[vs]));
         }
+        chunk_release(bars, i);
       }
       mma_commit(bar(bars->mma_done));
       mbar_drain(bar(bars->mma_done), 0);
@@ -646,7 +702,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     const int t = kTiles == 2 ? ((warp - 4) >> 2) & 1 : 0;    // tile of the block
     const int half = (warp - 4) >> (kTiles == 2 ? 3 : 2);     // columns [64 half, 64 half + 64)
     const int row = (tid - 128) & 127;                        // TMEM lane and row within the tile
-    const int st = tid - 128;                                 // index among the softmax threads
     const uint32_t lane_field = (uint32_t)((row & ~31) << 16);
     const uint32_t tS = tmem + lane_field + (t ? Cfg::kColS1 : Cfg::kColS0) + kC * half;
     const uint32_t tO = tmem + lane_field + (t ? Cfg::kColO1 : Cfg::kColO0);
@@ -659,20 +714,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     const bool pos_scale = c > 0.0f;
     const int tok_in_tile = p.by_group(row), head_in_group = row - tok_in_tile * p.G;
 
-    int4 split = make_int4(0, 0, 0, 0);  // the block that this piece hands on to the next one
-    Walk w;
-    for (begin(w); w.valid(); w.next(p)) {
+    for (uint32_t bi = 0;; ++bi) {
+      const ChunkBlock* block = chunk_take(bars, bi, ab);
+      // (both warps of a pair go on, or neither: they meet at its barrier)
+      if (!all_agree(block != nullptr, 4 + 4 * t + (row >> 5), 64)) break;
+      const ChunkBlock& w = *block;
       const int nv = w.v1 - w.v0;
       const int tile_tok = min(p.tq, w.ntok - t * p.tq);  // tokens of this tile (<= 0: no such tile)
       const int rows = tile_tok * p.G;                    // its rows
       const bool act = tile_tok > 0, live = (row & ~31) < rows;  // (live: some row of this warp)
-      const int pos = w.pos0(p.tq, t) + tok_in_tile;
+      const int pos_lo = w.pos0 + t * p.tq, pos_hi = pos_lo + tile_tok - 1;
+      const int pos = pos_lo + tok_in_tile;
       const bool mine = row < rows;
       const int kmax = (!mine || pos < 0) ? -1
-                       : p.win_r >= 0     ? (int)min((long long)w.s.n - 1, (long long)pos + p.win_r)
-                                          : w.s.n - 1;
+                       : p.win_r >= 0     ? (int)min((long long)w.n - 1, (long long)pos + p.win_r)
+                                          : w.n - 1;
       const int kmin = p.win_l >= 0 ? max(0, pos - p.win_l) : 0;
-      const int pos_lo = w.pos0(p.tq, t), pos_hi = pos_lo + tile_tok - 1;
       float m_run = -INFINITY, l_run = 0.0f, lr_run = 0.0f;
 
       for (int v = 0; act && v < nv; ++v) {
@@ -701,19 +758,29 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         for (int cc = 0; cc < kC; ++cc) x[cc] = __uint_as_float(r[cc >> 5][cc & 31]);
 
         const int k1 = key0 + 127, kbase = key0 + kC * half;
-        const bool all = pos_lo >= 0 && k1 < w.s.n && (p.win_r < 0 || k1 <= (long long)pos_lo + p.win_r) &&
+        const bool all = pos_lo >= 0 && k1 < w.n && (p.win_r < 0 || k1 <= (long long)pos_lo + p.win_r) &&
                          (p.win_l < 0 || key0 >= pos_hi - p.win_l || k1 < p.sinks);
-        if (!all) chunk_mask(x, kbase, kmin, kmax, p.sinks);
-        float m_tile = pos_scale ? fwd_tile_max<true>(x, false, 0, 0, 0, c) : -INFINITY;
-        if (!pos_scale) {
-          if (!all) {  // masked scores must stay -inf whatever the scale's sign
+        bool none = false;  // no score of this warp is visible
+        if (!all) {
+          uint32_t m[2];
+          chunk_visible(kbase, kmin, kmax, p.sinks, m);
+          none = __all_sync(0xffffffffu, (m[0] | m[1]) == 0u);
+          if (!none && !__all_sync(0xffffffffu, (m[0] & m[1]) == ~0u)) {
 #pragma unroll
-            for (int cc = 0; cc < kC; ++cc) x[cc] = x[cc] == -INFINITY ? -INFINITY : x[cc] * c;
-          } else {
-#pragma unroll
-            for (int cc = 0; cc < kC; ++cc) x[cc] *= c;
+            for (int cc = 0; cc < kC; ++cc) x[cc] = (m[cc >> 5] >> (cc & 31)) & 1u ? x[cc] : -INFINITY;
           }
-          for (int cc = 0; cc < kC; ++cc) m_tile = fmaxf(m_tile, x[cc]);
+        }
+        float m_tile = -INFINITY;
+        if (!none) {
+          if (pos_scale) {
+            m_tile = fwd_tile_max<true>(x, false, 0, 0, 0, c);
+          } else {  // masked scores stay -inf whatever the scale's sign
+#pragma unroll
+            for (int cc = 0; cc < kC; ++cc) {
+              x[cc] = x[cc] == -INFINITY && !all ? -INFINITY : x[cc] * c;
+              m_tile = fmaxf(m_tile, x[cc]);
+            }
+          }
         }
         {
           float* slot = xm + (xu & 1) * 256;
@@ -732,14 +799,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
           tc_fence_after_sync();
         }
         float2 sum = make_float2(0.0f, 0.0f), rsum = make_float2(0.0f, 0.0f);
+        if (none) {
+          uint32_t pk[16] = {};
 #pragma unroll
-        for (int q4 = 0; q4 < kC / 32; ++q4) {
-          uint32_t pk[16];
-          if (pos_scale)
-            chunk_exp<true>(x, q4 * 16, c, m_use, pk, sum, rsum);
-          else
-            chunk_exp<false>(x, q4 * 16, c, m_use, pk, sum, rsum);
-          tmem_st16(tP + q4 * 16, pk);
+          for (int q4 = 0; q4 < kC / 32; ++q4) tmem_st16(tP + q4 * 16, pk);
+        } else {
+#pragma unroll
+          for (int q4 = 0; q4 < kC / 32; ++q4) {
+            uint32_t pk[16];
+            if (pos_scale)
+              chunk_exp<true>(x, q4 * 16, c, m_use, pk, sum, rsum);
+            else
+              chunk_exp<false>(x, q4 * 16, c, m_use, pk, sum, rsum);
+            tmem_st16(tP + q4 * 16, pk);
+          }
         }
         l_run = l_run * alpha + (sum.x + sum.y);
         lr_run = lr_run * alpha + (rsum.x + rsum.y);
@@ -781,8 +854,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       }
 
       // ---- epilogue: O / (sum of the weights applied) and the log-sum-exp, final or partial
-      const bool whole = w.whole();
-      const int slot = 2 * (int)blockIdx.x + (w.start > w.u0 ? 1 : 0);  // of its partial: the piece's first block, or a later one
+      const bool whole = w.slot < 0;
       if (act) {
         mbar_wait(bar(bars->pv_done[t]), pvn & 1, ab);
         ++pvn;
@@ -797,9 +869,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         const float inv_l = l_o > 0.0f ? 1.0f / l_o : 0.0f;
         const float lse2 = l_tot > 0.0f ? m_run + lg2_approx(l_tot) : (l_tot == l_tot ? -INFINITY : l_tot);
         const bool dead = !(l_o > 0.0f) && l_o == l_o;  // no visible key (a NaN sum is not one)
-        const long long tok = (long long)w.s.c0 + w.i0 + t * p.tq + tok_in_tile;
+        const long long tok = (long long)w.c0 + t * p.tq + tok_in_tile;
         const int head = w.h * p.G + head_in_group;
-        const long long ptile = (long long)slot * kTiles + t;
+        const long long ptile = (long long)w.slot * kTiles + t;
         const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.pieces * kTiles * 128;
 #pragma unroll 1
         for (int cc = (D / 2) * half; cc < (D / 2) * (half + 1); cc += 32) {
@@ -841,13 +913,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         tc_fence_before_sync();
       }
       vn += nv;
-      if (!whole && w.start >= w.u0) {
-        const long long T = bars->th * p.Hkv;
-        const int last = ChunkSplit(T, (int)min((long long)p.pieces, T)).of(w.start + w.keys.cnt - 1);
-        split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * last + (slot & 1));
-      }
+      __syncwarp();
+      if (lane == 0) chunk_release(bars, bi);
     }
-    if (st == 0 && dbg_range(ab, blockIdx.x, 1, p.pieces)) p.split[blockIdx.x] = split;
   } else {
     if constexpr (kF8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kConvRegs) : "memory");
@@ -858,8 +926,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       const int c = ct % kPerRow;      // this thread's piece, in rows ct / kPerRow + k * kRowStep
       const int box_shift = 31 - __clz(p.box_rows);
       uint32_t n = 0;
-      Walk w;
-      for (begin(w); w.valid(); w.next(p)) {
+      const ChunkBlock* block;
+      for (uint32_t i = 0; (block = chunk_take(bars, i, ab)); ++i) {
+        const ChunkBlock& w = *block;
         for (int v = w.v0; v < w.v1; ++v) {
           const int key0 = w.keys.tile(v) * 128;
 #pragma unroll 1
@@ -913,6 +982,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
             }
           }
         }
+        __syncwarp();
+        if (lane == 0) chunk_release(bars, i);
       }
     }
   }
@@ -925,67 +996,52 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
 }
 
 // Joins the blocks that are spread over several pieces: CTA (r, y) takes the block that starts in
-// piece r and goes on, if there is one, and of it kRows rows. A row's partials are weighted by
-// 2^(their log-sum-exp - the largest), in piece order: the same sum in every run. Bound by the
-// latency of the partials, which lie in L2: those of a row are read sixteen at a time, ahead of the
-// log-sum-exps that weigh them, which the CTA reads together. The rows leave through shared memory,
-// whole. Launched as the main kernel's programmatic dependent: an SM takes it as soon as its CTA of
-// the main kernel is done.
-constexpr int kMergeThreads = 256, kMergeMaxPieces = 192;
-constexpr __host__ __device__ int merge_rows(int tiles) { return tiles == 2 ? 32 : 8; }
+// piece r and goes on, if there is one, and of it rows [8 y, 8 y + 8): a thread takes four columns of
+// one row. A row's partials are weighted by 2^(their log-sum-exp - the largest), in piece order: the
+// same sum in every run. Bound by the latency of the partials, which lie in L2: kBatch of them, with
+// their log-sum-exps, are on their way at once (few rows are spread over many pieces, two tiles of
+// rows over two or three). Launched as the main kernel's programmatic dependent: an SM takes it as
+// soon as its CTA of the main kernel is done.
+constexpr int kMergeThreads = 256, kMergeRows = 8;
 template <int D, int kTiles>
 __global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const ChunkParams p) {
-  constexpr int kRows = merge_rows(kTiles), kBatch = 16;
-  __shared__ uint2 sO[kRows][D / 4 + 1];
-  __shared__ float sL[kRows][kMergeMaxPieces];
+  constexpr int kBatch = kTiles == 2 ? 4 : 16;
   const Abort none{nullptr};
   griddep_wait();  // the pieces have been written
-  const int pf = blockIdx.x, tid = threadIdx.x;
+  const int pf = blockIdx.x;
   const int4 s = __ldcg(p.split + pf);
-  const int m = (s.w >> 1) - pf + 1, first = blockIdx.y * kRows, nrows = min(kRows, s.y * p.G - first);
-  if (nrows <= 0) return;
-  if (!dbg_range(none, pf, m, p.pieces) || m > kMergeMaxPieces) return;
-  // 128-row tile of partials i of the block, for its rows of tile 0 or 1; row in the tile
-  auto tile_of = [&](int i, int t) { return ((2LL * (pf + i) + (i == 0 ? (s.w & 1) : 0)) * kTiles + t) * 128; };
-  auto locate = [&](int rr, int& t, int& srow) {
-    t = p.by_group(rr) >= p.tq ? 1 : 0;
-    srow = rr - t * p.tq * p.G;
-  };
-  const int shift = nrows <= 1 ? 0 : 32 - __clz(nrows - 1);  // rows side by side: the next power of two
-  const int items = (D / 4) << shift;
-  float4 o4[kBatch];
-  auto fetch = [&](int e, int from) {
+  const int m = (s.w >> 1) - pf + 1, first = blockIdx.y * kMergeRows, nrows = min(kMergeRows, s.y * p.G - first);
+  if (nrows <= 0 || !dbg_range(none, pf, m, p.pieces)) return;
+  // a warp's threads: rows side by side (their number rounded up to a power of two), then columns
+  const int shift = nrows <= 1 ? 0 : 32 - __clz(nrows - 1);
+  for (int e = threadIdx.x; e < (D / 4) << shift; e += kMergeThreads) {
     const int rr = first + (e & ((1 << shift) - 1)), c4 = e >> shift;
-    int t, srow;
-    locate(rr, t, srow);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (from + i < m && rr - first < nrows)
-        o4[i] = __ldcg(reinterpret_cast<const float4*>(p.o_part + tile_of(from + i, t) * D) + c4 * 128 + srow);
-  };
-  if (tid < items) fetch(tid, 0);
-  for (int e = tid; e < nrows * m; e += kMergeThreads) {
-    const int i = e / nrows, rr = e - i * nrows;
-    int t, srow;
-    locate(first + rr, t, srow);
-    sL[rr][i] = __ldcg(p.lse_part + tile_of(i, t) + srow);
-  }
-  __syncthreads();
-  for (int e = tid; e < items; e += kMergeThreads) {
-    const int rr = e & ((1 << shift) - 1), c4 = e >> shift;
-    if (e != tid) fetch(e, 0);
-    if (rr >= nrows) continue;
-    float mx = -INFINITY;
-    for (int i = 0; i < m; ++i) mx = fmaxf(mx, sL[rr][i]);
-    const float m_sub = mx == -INFINITY ? 0.0f : mx;
-    float wsum = 0.0f;
+    if (rr - first >= nrows) continue;
+    const int itok = p.by_group(rr), t = itok >= p.tq ? 1 : 0, srow = rr - t * p.tq * p.G;
+    float mx = -INFINITY, wsum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int from = 0; from < m; from += kBatch) {
-      if (from > 0) fetch(e, from);
+      float4 o4[kBatch];
+      float lse[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
+        lse[i] = -INFINITY;
+        o4[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (from + i >= m) continue;
-        const float w = ex2_approx(sL[rr][from + i] - m_sub);
+        const long long tile = (2LL * (pf + from + i) + (from + i == 0 ? (s.w & 1) : 0)) * kTiles + t;
+        lse[i] = __ldcg(p.lse_part + tile * 128 + srow);
+        o4[i] = __ldcg(reinterpret_cast<const float4*>(p.o_part + tile * 128 * D) + c4 * 128 + srow);
+      }
+      float most = mx;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) most = fmaxf(most, lse[i]);
+      const float ref = most == -INFINITY ? 0.0f : most, down = ex2_approx(mx - ref);  // (0 at first)
+      wsum *= down;
+      acc = make_float4(acc.x * down, acc.y * down, acc.z * down, acc.w * down);
+      mx = most;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float w = ex2_approx(lse[i] - ref);
         wsum += w;
         acc.x = fmaf(w, o4[i].x, acc.x);
         acc.y = fmaf(w, o4[i].y, acc.y);
@@ -994,19 +1050,14 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const Chu
       }
     }
     const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
-    sO[rr][c4] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (c4 == 0) {
-      const int itok = p.by_group(first + rr);
-      const long long li = (long long)(s.z * p.G + first + rr - itok * p.G) * p.total + s.x + itok;
-      if (dbg_range(none, li, 1, (long long)p.Hq * p.total))
-        p.lse[li] = wsum == 0.0f ? -INFINITY : (m_sub + lg2_approx(wsum)) * kLn2;
-    }
-  }
-  __syncthreads();
-  for (int e = tid; e < nrows * (D / 4); e += kMergeThreads) {
-    const int rr = e / (D / 4), c4 = e % (D / 4), itok = p.by_group(first + rr);
-    const long long oi = ((long long)(s.x + itok) * p.Hq + s.z * p.G + first + rr - itok * p.G) * D + c4 * 4;
-    if (dbg_range(none, oi, 4, (long long)p.total * p.Hq * D)) *reinterpret_cast<uint2*>(p.o + oi) = sO[rr][c4];
+    const int head = s.z * p.G + rr - itok * p.G;
+    const long long tok = (long long)s.x + itok, oi = (tok * p.Hq + head) * D + c4 * 4;
+    const long long li = (long long)head * p.total + tok;
+    if (dbg_range(none, oi, 4, (long long)p.total * p.Hq * D))
+      *reinterpret_cast<uint2*>(p.o + oi) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (c4 == 0 && dbg_range(none, li, 1, (long long)p.Hq * p.total))
+      p.lse[li] = wsum == 0.0f ? -INFINITY : ((mx == -INFINITY ? 0.0f : mx) + lg2_approx(wsum)) * kLn2;
   }
 }
 

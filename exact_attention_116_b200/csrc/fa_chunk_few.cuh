@@ -45,7 +45,7 @@ struct FewCfg {
   static constexpr int kOffW = kOffQ + 2 * kQBytes;
   static constexpr int kOffX = kOffW + 2 * kWBytes;         // maxima and sums: [warp][row], three of them
   static constexpr int kOffBar = kOffX + 1024;
-  static constexpr int kSmemBytes = kOffBar + 1024 + 1024;
+  static constexpr int kSmemBytes = kOffBar + 1536 + 1024;
   static constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 128;  // S: two buffers of 16 columns
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
@@ -54,6 +54,7 @@ struct FewBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[2][kFewSlots], empty[2][kFewSlots];  // K, V tiles
   uint64_t s_full[2], s_empty[2], w_full[2], pv_done[2];
+  uint64_t block_full[kBlockRing], block_empty[kBlockRing];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
@@ -62,6 +63,7 @@ struct FewBars {
   ChunkSeq first_seq;
   long long sums[3][4];
   int many[4];
+  ChunkBlock block[kBlockRing];
   float q_factor[2][kFewRows];  // log2 score per unit of S, before the key's scale
 };
 
@@ -112,9 +114,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
                         const __nv_bfloat16* __restrict__ q, long long q_stride, const ChunkParams p) {
   using Cfg = FewCfg;
-  using Walk = ChunkWalk<1>;
   constexpr int D = kFewD, kPairs = kFewRows / 2;
-  static_assert(sizeof(FewBars) <= 1024, "barrier block");
+  static_assert(sizeof(FewBars) <= 1536, "barrier block");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       else if (i < 4) count = 5;                               // q_empty: the MMAs, the softmax warps
       else if (i >= kEmptyK && i < kEmptyK + kFewSlots) count = 5;  // K tile: the same (its scales)
       else if (i >= kS + 2 && i < kS + 6) count = 4;           // s_empty, w_full: the softmax warps
+      else if (i >= kBars - 1 - kBlockRing && i < kBars - 1) count = 10;  // block_empty: loads, MMAs, softmax, queries
       if (i < kBars) mbar_init(first + i * 8, count);
     }
     fence_barrier_init();
@@ -171,8 +173,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const bool loads = grp < groups, scales = lane >= 16;
     const uint32_t box_off = (uint32_t)grp * p.box_rows;
     uint32_t n = 0;
-    Walk w;
-    for (w.begin(p, bars); w.valid() && !ab.raised(); w.next(p)) {
+    const ChunkBlock* block;
+    for (uint32_t bi = 0; (block = chunk_take(bars, bi, ab)) && !ab.raised(); ++bi) {
+      const ChunkBlock& w = *block;
       auto place = [&](int v, int& page, int& row) {
         const int key = w.keys.tile(v) * 128 + (int)box_off, last = key + p.box_rows - 1;
         page = p.num_pages;
@@ -215,10 +218,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         if (!ok) break;
       }
+      __syncwarp();
+      if (lane == 0) chunk_release(bars, bi);
     }
     for (uint32_t i = n > kFewSlots ? n - kFewSlots : 0; i < n; ++i)  // every load issued lands before the CTA exits
       for (int kv = 0; kv < 2; ++kv) mbar_drain(bar(bars->full[kv][i % kFewSlots]), (i / kFewSlots) & 1);
   } else if (warp == 3) {
+    if (lane == 0) chunk_publish<1>(p, bars, ab);
+  } else if (warp == 2) {
     if (blockIdx.x == 0)
       report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, lane, 32);
   } else if (warp == 1) {
@@ -243,8 +250,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mma_commit(bar(bars->empty[0][slot]));
         if (last) mma_commit(bar(bars->q_empty[qb]));
       };
-      Walk w;
-      for (w.begin(p, bars); w.valid(); w.next(p), ++blocks) {
+      const ChunkBlock* block;
+      for (; (block = chunk_take(bars, blocks, ab)); ++blocks) {
+        const ChunkBlock& w = *block;
         const int nv = w.v1 - w.v0;
         const uint32_t qb = blocks & 1;
         mbar_wait(bar(bars->q_full[qb]), (blocks >> 1) & 1, ab);
@@ -264,6 +272,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           mma_commit(bar(bars->pv_done[buf]));
           mma_commit(bar(bars->empty[1][slot]));
         }
+        chunk_release(bars, blocks);
       }
       mma_commit(bar(bars->mma_done));
       mbar_drain(bar(bars->mma_done), 0);
@@ -277,15 +286,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     int* sE = reinterpret_cast<int*>(smem_gen + Cfg::kOffX + 768);  // [warp]
     const uint32_t w_at = (uint32_t)key_in;  // byte of this key in a row of W, before the swizzle
     uint32_t n = 0, blocks = 0;
-    int4 split = make_int4(0, 0, 0, 0);  // the block that this piece hands on to the next one
     auto pv_wait = [&](uint32_t i) {     // W V of tile i has been added
       mbar_wait(bar(bars->pv_done[i & 1]), (i >> 1) & 1, ab);
       tc_fence_after_sync();
     };
-    Walk w;
-    for (w.begin(p, bars); w.valid(); w.next(p), ++blocks) {
+    for (;; ++blocks) {
+      const ChunkBlock* block = chunk_take(bars, blocks, ab);
+      if (!all_agree(block != nullptr, 2, 128)) break;  // (the warps meet at this barrier: all go on, or none)
+      const ChunkBlock& w = *block;
       const int nv = w.v1 - w.v0, rows = w.ntok * p.G, pairs = (rows + 1) >> 1;
-      const int pos0 = w.pos0(p.tq, 0), pos1 = pos0 + w.ntok - 1;
+      const int pos0 = w.pos0, pos1 = pos0 + w.ntok - 1, keys = w.n;
       const uint32_t qb = blocks & 1;
       float2 c2[kPairs], m2[kPairs], l2[kPairs], lr2[kPairs];
       mbar_wait(bar(bars->q_full[qb]), (blocks >> 1) & 1, ab);
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const float kf = ks == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float((int)max(ks, 1u) << 23);
 
         // scores against the references, -inf where masked; is the key seen at all?
-        const bool all = pos0 >= 0 && key0 + 127 < w.s.n &&
+        const bool all = pos0 >= 0 && key0 + 127 < keys &&
                          (p.win_r < 0 || key0 + 127 <= (long long)pos0 + p.win_r) &&
                          (p.win_l < 0 || key0 >= pos1 - p.win_l || key0 + 127 < p.sinks);
         bool seen = true;
@@ -349,7 +359,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int pos = pos0 + p.by_group(2 * i + e);
-              const bool vis = pos >= 0 && key < w.s.n && (p.win_r < 0 || key <= (long long)pos + p.win_r) &&
+              const bool vis = pos >= 0 && key < keys && (p.win_r < 0 || key <= (long long)pos + p.win_r) &&
                                (p.win_l < 0 || key >= pos - p.win_l || key < p.sinks) && 2 * i + e < rows;
               seen |= vis;
               if (!vis) (e ? a[i].y : a[i].x) = -INFINITY;
@@ -458,8 +468,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
 
       // ---- epilogue: this thread's column of every row
-      const bool whole = w.whole();
-      const int slot = 2 * (int)blockIdx.x + (w.start > w.u0 ? 1 : 0);  // of its partial
+      const bool whole = w.slot < 0;
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         if (i >= pairs) break;
@@ -505,14 +514,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const float m = (i & 1) ? m2[r >> 1].y : m2[r >> 1].x;
           const float lse2 = l > 0.0f ? m + lg2_approx(l) : (l == l ? -INFINITY : l);
           const int itok = p.by_group(r), head = w.h * p.G + r - itok * p.G;
-          const long long tok = (long long)w.s.c0 + w.i0 + itok;
+          const long long tok = (long long)w.c0 + itok;
           if (whole) {
             const long long oi = (tok * p.Hq + head) * D + key_in, li = (long long)head * p.total + tok;
             if (dbg_range(ab, oi, 1, o_size)) p.o[oi] = __float2bfloat16_rn(value);
             if (key_in == 0 && dbg_range(ab, li, 1, (long long)p.Hq * p.total))
               p.lse[li] = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
           } else {
-            const long long pi = (long long)slot * 128;
+            const long long pi = (long long)w.slot * 128;
             if (dbg_range(ab, pi + r, 1, part_rows)) {
               p.o_part[pi * D + ((key_in >> 2) * 128 + r) * 4 + (key_in & 3)] = value;
               if (key_in == 0) p.lse_part[pi + r] = lse2;
@@ -522,22 +531,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       tc_fence_before_sync();
       named_bar_sync(2, 128);  // the sums have been read
-      if (!whole && w.start >= w.u0) {
-        const long long T = bars->th * p.Hkv;
-        const int last = ChunkSplit(T, (int)min((long long)p.pieces, T)).of(w.start + w.keys.cnt - 1);
-        split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * last + (slot & 1));
-      }
+      if (lane == 0) chunk_release(bars, blocks);
     }
-    if (key_in == 0 && dbg_range(ab, blockIdx.x, 1, p.pieces)) p.split[blockIdx.x] = split;
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- queries: eight threads a row, 16 elements each
     const int ct = tid - 256, row = ct >> 3, c = ct & 7;
     uint32_t blocks = 0;
-    Walk w;
-    for (w.begin(p, bars); w.valid(); w.next(p), ++blocks) {
+    const ChunkBlock* block;
+    for (; (block = chunk_take(bars, blocks, ab)); ++blocks) {
+      const ChunkBlock& w = *block;
       const uint32_t qb = blocks & 1;
       const int itok = p.by_group(row), head = w.h * p.G + row - itok * p.G;
-      const long long qi = ((long long)w.s.c0 + w.i0 + itok) * q_stride + (long long)head * D + c * 16;
+      const long long qi = ((long long)w.c0 + itok) * q_stride + (long long)head * D + c * 16;
       uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
       if (row < w.ntok * p.G) {
         x[0] = __ldg(reinterpret_cast<const uint4*>(q + qi));
@@ -570,6 +575,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (c == 0) bars->q_factor[qb][row] = p.scale_log2 * exp2_int(-up);
       fence_proxy_async_smem();
       mbar_arrive(bar(bars->q_full[qb]));
+      __syncwarp();
+      if (lane == 0) chunk_release(bars, blocks);
     }
   }
 

@@ -8,8 +8,10 @@ raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 
 import torch
 
@@ -20,7 +22,8 @@ FA_OK = 0
 STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
                 4: "FA_ERR_TIMEOUT", 5: "FA_ERR_NO_MEMORY", 6: "FA_ERR_DEVICE"}
 EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_varlen", "fa_fwd_fp8", "fa_decode_splits", "fa_decode_workspace_bytes", "fa_decode_paged",
-           "fa_cache_write", "fa_cache_read", "fa_chunk_workspace_bytes", "fa_chunk_paged", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_ex", "fa_bwd_varlen", "fa_bwd_deterministic", "fa_bwd_preprocess",
+           "fa_cache_write", "fa_cache_read", "fa_cache_write_args", "fa_cache_read_args", "fa_chunk_workspace_bytes",
+           "fa_chunk_paged", "fa_chunk_paged_args", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_ex", "fa_bwd_varlen", "fa_bwd_deterministic", "fa_bwd_preprocess",
            "fa_bwd_main", "fa_bwd_dq_convert", "fa_bwd_static_workspace", "fa_check", "fa_status_string")
 
 _lib = None
@@ -66,6 +69,9 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.fa_chunk_workspace_bytes.restype = sz
     lib.fa_chunk_paged.argtypes = [vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, i, i, i, vp, sz,
                                    vp]
+    for name in ("fa_cache_write_args", "fa_cache_read_args", "fa_chunk_paged_args"):
+        getattr(lib, name).argtypes = [ctypes.c_char_p]
+        getattr(lib, name).restype = i
     lib.fa_bwd_workspace_bytes.argtypes = [i, i, i, i]
     lib.fa_bwd_workspace_bytes.restype = sz
     lib.fa_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i, i, vp, sz, vp]
@@ -440,18 +446,26 @@ def _cuda_index(t: torch.Tensor) -> int:
     return index
 
 
-def _launch(name: str, index: int, stream, *args) -> None:
-    """Call the C function on device `index` (it launches on the current device), on `stream` or that
-    device's current one."""
-    fn = getattr(load(), name)
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+# fa_cache_args and fa_chunk_args: one packed structure takes a quarter of the time of as many ctypes arguments
+_CACHE_ARGS = struct.Struct("@10Pq7i0P")
+_CHUNK_ARGS = struct.Struct("@12PNq12if0P")
+
+
+def _launch(name: str, index: int, packed: bytes) -> None:
+    """Call the C function with its packed arguments on device `index` (it launches on the current device)."""
+    fn = getattr(load(), name + "_args")
     if index == torch.cuda.current_device():
-        status = fn(*args, handle)
+        status = fn(packed)
     else:
         with torch.cuda.device(index):
-            status = fn(*args, handle)
+            status = fn(packed)
     if status != FA_OK:
         _raise(status, name)
+
+
+def _stream_on(index: int, stream) -> int:
+    """The stream's handle; None: the current stream of device `index`."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _check_rows(t: torch.Tensor, name: str, index: int, heads: int | None, d: int) -> int:
@@ -476,34 +490,52 @@ _E8M0 = (torch.uint8, torch.float8_e8m0fnu)
 
 def _check_cache(index: int, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens):
     """Pages, scales, block table, lengths and offsets of a ragged batch on device `index`; returns (B, H, d,
-    num_pages, page_size, max_pages, k_scale pointer, v_scale pointer)."""
+    num_pages, page_size, max_pages, k_scale pointer, v_scale pointer), the pointers 0 without scales."""
+    shape, kind, i32 = k_cache.shape, k_cache.dtype, torch.int32
+    if not (len(shape) == 4 and shape == v_cache.shape and kind == v_cache.dtype and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and k_cache.get_device() == v_cache.get_device() == index
+            and block_table.get_device() == seqlens.get_device() == cu_seqlens.get_device() == index
+            and block_table.dtype == i32 and seqlens.dtype == i32 and cu_seqlens.dtype == i32
+            and block_table.is_contiguous() and seqlens.is_contiguous() and cu_seqlens.is_contiguous()
+            and (kind == torch.bfloat16 and k_scale is None if v_scale is None else kind in _E4M3)):
+        _refuse_cache(index, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens)
+    num_pages, page_size, H, d = shape
+    ks = vs = 0
+    if v_scale is not None:
+        if k_scale is None or not (
+                k_scale.dtype in _E8M0 and v_scale.dtype in _E8M0 and k_scale.is_contiguous() and v_scale.is_contiguous()
+                and k_scale.get_device() == v_scale.get_device() == index
+                and k_scale.shape == v_scale.shape == (num_pages, H, page_size)):
+            _refuse_cache(index, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    B, table = seqlens.numel(), block_table.shape
+    if seqlens.dim() != 1 or len(table) != 2 or table[0] != B or cu_seqlens.dim() != 1 or cu_seqlens.numel() != B + 1:
+        raise ValueError("block_table must be (B, max_pages), seqlens (B,) and cu_seqlens (B + 1,)")
+    return B, H, d, num_pages, page_size, table[1], ks, vs
+
+
+def _refuse_cache(index, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens):
+    """Says what is wrong with a batch that _check_cache refuses."""
     quantised = k_scale is not None
     if quantised != (v_scale is not None):
         raise ValueError("give both k_scale and v_scale (E4M3 pages), or neither (bfloat16 pages)")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be (num_pages, page_size, heads, head_dim), of equal shape and type")
     kinds = _E4M3 if quantised else (torch.bfloat16,)
-    shape = k_cache.shape
-    if len(shape) != 4 or shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must be (num_pages, page_size, heads, head_dim), of equal shape")
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if t.dtype not in kinds or not t.is_contiguous() or t.get_device() != index:
             raise ValueError(f"{name} must be contiguous, on the rows' device and {' or '.join(map(str, kinds))} "
                              f"({'with' if quantised else 'without'} scales)")
-    num_pages, page_size, H, d = shape
-    ks = vs = None
-    if quantised:
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t.dtype not in _E8M0 or not t.is_contiguous() or t.get_device() != index or \
-                    t.shape != (num_pages, H, page_size):
-                raise ValueError(f"{name} must be a contiguous (num_pages, heads, page_size) tensor of E8M0 bytes "
-                                 "(uint8 or float8_e8m0fnu) on the rows' device")
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    num_pages, page_size, H, _ = k_cache.shape
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")) if quantised else ():
+        if t.dtype not in _E8M0 or not t.is_contiguous() or t.get_device() != index or \
+                t.shape != (num_pages, H, page_size):
+            raise ValueError(f"{name} must be a contiguous (num_pages, heads, page_size) tensor of E8M0 bytes "
+                             "(uint8 or float8_e8m0fnu) on the rows' device")
     for t, name in ((block_table, "block_table"), (seqlens, "seqlens"), (cu_seqlens, "cu_seqlens")):
         if t.dtype != torch.int32 or not t.is_contiguous() or t.get_device() != index:
             raise ValueError(f"{name} must be a contiguous int32 tensor on the rows' device")
-    B = seqlens.numel()
-    if seqlens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B or cu_seqlens.shape != (B + 1,):
-        raise ValueError("block_table must be (B, max_pages), seqlens (B,) and cu_seqlens (B + 1,)")
-    return B, H, d, num_pages, page_size, block_table.shape[1], ks, vs
+    raise ValueError("the paged cache, its scales, block table, lengths and offsets do not fit together")
 
 
 def cache_write_paged(k_new, v_new, k_cache, v_cache, block_table, seqlens, cu_seqlens, k_scale=None, v_scale=None,
@@ -519,9 +551,10 @@ def cache_write_paged(k_new, v_new, k_cache, v_cache, block_table, seqlens, cu_s
     stride = _check_rows(k_new, "k_new", index, H, d)
     if v_new.shape != k_new.shape or _check_rows(v_new, "v_new", index, H, d) != stride:
         raise ValueError("v_new must have the shape and row stride of k_new")
-    _launch("fa_cache_write", index, stream, k_new.data_ptr(), v_new.data_ptr(), stride, k_cache.data_ptr(),
-            v_cache.data_ptr(), ks, vs, block_table.data_ptr(), seqlens.data_ptr(), cu_seqlens.data_ptr(), B,
-            k_new.shape[0], H, d, num_pages, page_size, max_pages)
+    _launch("fa_cache_write", index, _CACHE_ARGS.pack(
+        k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(),
+        seqlens.data_ptr(), cu_seqlens.data_ptr(), _stream_on(index, stream), stride, B, k_new.shape[0], H, d, num_pages,
+        page_size, max_pages))
 
 
 def cache_read_paged_into(k_cache, v_cache, block_table, seqlens, cu_seqlens, k, v, k_scale=None, v_scale=None,
@@ -534,9 +567,10 @@ def cache_read_paged_into(k_cache, v_cache, block_table, seqlens, cu_seqlens, k,
     stride = _check_rows(k, "k", index, H, d)
     if v.shape != k.shape or _check_rows(v, "v", index, H, d) != stride:
         raise ValueError("v must have the shape and row stride of k")
-    _launch("fa_cache_read", index, stream, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(),
-            seqlens.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), stride, B, k.shape[0], H, d,
-            num_pages, page_size, max_pages)
+    _launch("fa_cache_read", index, _CACHE_ARGS.pack(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(),
+        seqlens.data_ptr(), cu_seqlens.data_ptr(), _stream_on(index, stream), stride, B, k.shape[0], H, d, num_pages,
+        page_size, max_pages))
 
 
 def cache_read_paged(k_cache, v_cache, block_table, seqlens, cu_seqlens, total, k_scale=None, v_scale=None,
@@ -545,19 +579,27 @@ def cache_read_paged(k_cache, v_cache, block_table, seqlens, cu_seqlens, total, 
     if total is larger, are not initialised)."""
     if k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be (num_pages, page_size, heads, head_dim), of equal shape")
-    k = k_cache.new_empty((total, *k_cache.shape[2:]), dtype=torch.bfloat16)
+    H, d = k_cache.shape[2:]
+    k = torch.empty_strided((total, H, d), (max(H * d, 1), max(d, 1), 1), dtype=torch.bfloat16, device=k_cache.device)
     v = torch.empty_like(k)
-    _used_on(stream, k, v)
+    if stream is not None:
+        _used_on(stream, k, v)
     cache_read_paged_into(k_cache, v_cache, block_table, seqlens, cu_seqlens, k, v, k_scale, v_scale, stream)
     return k, v
 
 
+def _int32(x, name: str) -> int:
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits (got {x})")
+    return x
+
+
 def _used_on(stream, *new: torch.Tensor) -> None:
-    """Tensors made here are not handed out again before work on `stream` (None: the current one) is done."""
-    if stream is not None:
-        for t in new:
-            if t.is_cuda:
-                t.record_stream(stream)
+    """Tensors made here are not handed out again before work on `stream` is done."""
+    for t in new:
+        if t.is_cuda:
+            t.record_stream(stream)
 
 
 def chunk_workspace_bytes(B: int, total: int, Hq: int, Hkv: int, d: int) -> int:
@@ -565,6 +607,7 @@ def chunk_workspace_bytes(B: int, total: int, Hq: int, Hkv: int, d: int) -> int:
     return int(load().fa_chunk_workspace_bytes(B, total, Hq, Hkv, d))
 
 
+@functools.lru_cache(maxsize=4096)
 def _chunk_workspace(index: int, *sizes: int) -> int:
     if index == torch.cuda.current_device():
         return chunk_workspace_bytes(*sizes)
@@ -590,15 +633,20 @@ def chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, l
     if Hq == 0 or Hkv == 0 or Hq % Hkv:
         raise ValueError(f"the {Hq} query heads must be a multiple of the cache's {Hkv}")
     if workspace is None:
-        workspace = o.new_empty(_chunk_workspace(index, B, total, Hq, Hkv, d), dtype=torch.uint8)
-        _used_on(stream, workspace)
-    elif workspace.get_device() != index:
-        raise ValueError("workspace must be on q's device")
-    ws, wb = _check_workspace(workspace)
-    _launch("fa_chunk_paged", index, stream, q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
-            block_table.data_ptr(), seqlens.data_ptr(), cu_seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, total, Hq,
-            Hkv, d, num_pages, page_size, max_pages, _scale(scale, d), 1 if causal else 0, int(window[0]),
-            int(window[1]), int(sinks), ws, wb)
+        wb = _chunk_workspace(index, B, total, Hq, Hkv, d)
+        workspace = torch.empty_strided((wb,), (1,), dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            _used_on(stream, workspace)
+        ws = workspace.data_ptr()
+    else:
+        if workspace.get_device() != index:
+            raise ValueError("workspace must be on q's device")
+        ws, wb = _check_workspace(workspace)
+    _launch("fa_chunk_paged", index, _CHUNK_ARGS.pack(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(), seqlens.data_ptr(),
+        cu_seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), ws, _stream_on(index, stream), wb, stride, B, total, Hq, Hkv, d,
+        num_pages, page_size, max_pages, 1 if causal else 0, _int32(window[0], "window"), _int32(window[1], "window"),
+        _int32(sinks, "sinks"), _scale(scale, d)))
 
 
 def attention_chunk_paged(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, scale=None, causal=False,
@@ -613,8 +661,10 @@ def attention_chunk_paged(q, k_cache, v_cache, block_table, seqlens, cu_seqlens,
     if q.dim() != 3:
         raise ValueError("q must be a (total, heads, head_dim) bfloat16 CUDA tensor")
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
-    lse = q.new_empty((q.shape[1], q.shape[0]), dtype=torch.float32)
-    _used_on(stream, o, lse)
+    total, Hq, _ = q.shape
+    lse = torch.empty_strided((Hq, total), (max(total, 1), 1), dtype=torch.float32, device=q.device)
+    if stream is not None:
+        _used_on(stream, o, lse)
     chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, lse, scale, causal, window, sinks,
                      k_scale, v_scale, None, stream)
     return o, lse

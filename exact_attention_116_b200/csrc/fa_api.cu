@@ -1169,6 +1169,28 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   return st;
 }
 
+int fa_cache_write_args(const fa_cache_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_cache_write(a->k_rows, a->v_rows, a->row_stride, a->k_cache, a->v_cache, a->k_scale, a->v_scale,
+                        a->block_table, a->seqlens, a->cu_seqlens, a->B, a->total, a->H, a->d, a->num_pages,
+                        a->page_size, a->max_pages, a->stream);
+}
+
+int fa_cache_read_args(const fa_cache_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_cache_read(a->k_cache, a->v_cache, a->k_scale, a->v_scale, a->block_table, a->seqlens, a->cu_seqlens,
+                       const_cast<void*>(a->k_rows), const_cast<void*>(a->v_rows), a->row_stride, a->B, a->total, a->H,
+                       a->d, a->num_pages, a->page_size, a->max_pages, a->stream);
+}
+
+int fa_chunk_paged_args(const fa_chunk_args* a) {
+  if (!a) return FA_ERR_INVALID_ARG;
+  return fa_chunk_paged(a->q, a->q_stride, a->k_cache, a->v_cache, a->k_scale, a->v_scale, a->block_table, a->seqlens,
+                        a->cu_seqlens, a->o, a->lse, a->B, a->total, a->Hq, a->Hkv, a->d, a->num_pages, a->page_size,
+                        a->max_pages, a->scale, a->causal, a->win_l, a->win_r, a->sinks, a->workspace,
+                        a->workspace_bytes, a->stream);
+}
+
 int fa_bwd_preprocess(const void* o, const float* lse, const void* dO, int B, int N, int H, int d, void* workspace,
                       size_t workspace_bytes_, fa_stream_t stream) {
   int wl = -1, wr = -1;

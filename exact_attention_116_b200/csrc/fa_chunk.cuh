@@ -544,21 +544,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     const uint32_t box_off = (uint32_t)grp * p.box_rows;
     uint32_t n = 0, qn[2] = {0, 0};  // K/V tiles issued, Q tiles issued
     constexpr int kRing = kF8 ? Cfg::kRawSlots : Cfg::kSlots;
-    // page and row of this lane's box of tile v of block w; page num_pages: zeros
+    // page and row of this lane's box of tile v of block w; row -1: no page (zeros)
     auto place = [&](const ChunkBlock& w, int v, int& page, int& row) {
       const int key = w.keys.tile(v) * 128 + (int)box_off, last = key + p.box_rows - 1;
-      page = p.num_pages;
-      row = 0;
+      row = -1;  // no page
       if (!loads || key > w.keys.vis_hi || (last < w.keys.vis_lo && key >= p.sinks)) return;
       const int in_seq = p.by_page(key);
       const long long ti = (long long)w.b * p.max_pages + in_seq;
       if (!dbg_range(ab, ti, 1, (long long)p.B * p.max_pages)) return;
       page = __ldg(p.block_table + ti);
       row = key - in_seq * p.page_size;
-      if (page < 0 || page >= p.num_pages) {
-        atomicOr(&g_fa_error, kErrBadInput);
-        page = p.num_pages;
-      }
     };
     int page = 0, row = 0;
     const ChunkBlock* block;
@@ -585,7 +580,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       place(w, w.v0, page, row);
       const int h = w.h;
       for (int v = w.v0; v < w.v1 && !ab.raised(); ++v) {
-        const int pg = page, rw = row;
+        // (looked at only now: the entry was read while the tile before was loaded)
+        int pg = p.num_pages, rw = 0;
+        if (row >= 0) {
+          if (page >= 0 && page < p.num_pages) {
+            pg = page;
+            rw = row;
+          } else {
+            atomicOr(&g_fa_error, kErrBadInput);
+          }
+        }
         if (v + 1 < w.v1) place(w, v + 1, page, row);  // the next tile's page, read while this one waits
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++n) {

@@ -178,23 +178,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const ChunkBlock& w = *block;
       auto place = [&](int v, int& page, int& row) {
         const int key = w.keys.tile(v) * 128 + (int)box_off, last = key + p.box_rows - 1;
-        page = p.num_pages;
-        row = 0;
+        row = -1;  // no page
         if (!loads || key > w.keys.vis_hi || (last < w.keys.vis_lo && key >= p.sinks)) return;
         const int in_seq = p.by_page(key);
         const long long ti = (long long)w.b * p.max_pages + in_seq;
         if (!dbg_range(ab, ti, 1, (long long)p.B * p.max_pages)) return;
         page = __ldg(p.block_table + ti);
         row = key - in_seq * p.page_size;
-        if (page < 0 || page >= p.num_pages) {
-          atomicOr(&g_fa_error, kErrBadInput);
-          page = p.num_pages;
-        }
       };
-      int page, row;
+      int page = 0, row = 0;
       place(w.v0, page, row);
       for (int v = w.v0; v < w.v1 && !ab.raised(); ++v, ++n) {
-        const int pg = page, rw = row;
+        // (looked at only now: the entry was read while the tile before was loaded)
+        int pg = p.num_pages, rw = 0;
+        if (row >= 0) {
+          if (page >= 0 && page < p.num_pages) {
+            pg = page;
+            rw = row;
+          } else {
+            atomicOr(&g_fa_error, kErrBadInput);
+          }
+        }
         if (v + 1 < w.v1) place(v + 1, page, row);  // the next tile's page, read while this one waits
         const uint32_t slot = n % kFewSlots, phase = (n / kFewSlots) & 1;
         bool ok = true;

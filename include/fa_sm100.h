@@ -244,6 +244,36 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
                    fa_stream_t stream);
 
 /*
+ * The same calls with their arguments in a structure, for callers to whom many arguments are dear
+ * (the Python binding): each field is the argument of that name. fa_cache_read_args takes the rows
+ * it writes in k_rows and v_rows.
+ */
+typedef struct {
+  const void *k_rows, *v_rows;
+  void *k_cache, *v_cache, *k_scale, *v_scale;
+  const int *block_table, *seqlens, *cu_seqlens;
+  fa_stream_t stream;
+  long long row_stride;
+  int B, total, H, d, num_pages, page_size, max_pages;
+} fa_cache_args;
+int fa_cache_write_args(const fa_cache_args* args);
+int fa_cache_read_args(const fa_cache_args* args);
+
+typedef struct {
+  const void *q, *k_cache, *v_cache, *k_scale, *v_scale;
+  const int *block_table, *seqlens, *cu_seqlens;
+  void* o;
+  float* lse;
+  void* workspace;
+  fa_stream_t stream;
+  size_t workspace_bytes;
+  long long q_stride;
+  int B, total, Hq, Hkv, d, num_pages, page_size, max_pages, causal, win_l, win_r, sinks;
+  float scale;
+} fa_chunk_args;
+int fa_chunk_paged_args(const fa_chunk_args* args);
+
+/*
  * Bytes of device workspace fa_bwd needs: a float32 dQ accumulator (B,N,H,d), two
  * float32 (B,H,ceil(N/128)*128) row vectors (-LSE*log2(e) and -D, D = rowsum(dO*O)) and a
  * 256-byte block holding the work counter of the main kernel, each region 256-byte

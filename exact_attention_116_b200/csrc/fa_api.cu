@@ -682,6 +682,16 @@ fa::FastDiv fast_div(unsigned d) {
 // Rows of a few tokens over E4M3 pages take the transposed kernel: when a sequence's rows fit its
 // 16-row blocks on average (a longer chunk in such a batch is cut into several, which read its keys
 // again).
+// Heads whose CTAs run next to each other: the most of 4, 2 and 1 that divides the heads and the SMs.
+#ifndef FA_HG
+#define FA_HG 4
+#endif
+int chunk_head_group(int Hkv, int sms) {
+  for (int hg = FA_HG; hg > 1; hg /= 2)
+    if (Hkv % hg == 0 && sms % hg == 0) return hg;
+  return 1;
+}
+
 bool chunk_few(bool f8, int d, int B, int total, int G) {
   return f8 && d == fa::kFewD && G <= fa::kFewRows && (double)total <= (double)B * (fa::kFewRows / G);
 }
@@ -704,10 +714,10 @@ int chunk_launch(int grid, const CUtensorMap* m, const fa::ChunkParams& p, cudaS
 
 // The join of blocks that are spread over several pieces, as the main kernel's programmatic dependent.
 template <int D, int kTiles>
-int chunk_merge_launch(int pieces, const fa::ChunkParams& p, cudaStream_t stream) {
+int chunk_merge_launch(int ctas, const fa::ChunkParams& p, cudaStream_t stream) {
   const long long rows = std::min<long long>((long long)p.total * p.G, kTiles * 128);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pieces, (unsigned)((rows + fa::kMergeRows - 1) / fa::kMergeRows));
+  cfg.gridDim = dim3(ctas, (unsigned)((rows + fa::kMergeRows - 1) / fa::kMergeRows));
   cfg.blockDim = dim3(fa::kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1101,11 +1111,12 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
         overlap(workspace, ws.n, o, ob) || overlap(workspace, ws.n, lse, lb))
       return FA_ERR_INVALID_ARG;
   }
-  // pieces: one per SM, and no more than the key tiles there can be
+  // CTAs: one per SM, and no more than the key tiles there can be; heads in groups (fa_chunk.cuh)
+  const int hg = chunk_head_group(Hkv, sms);
   const double blocks = (double)(total / ((few ? 1 : tiles) * tq)) + std::min(B, total);
   const int key_tiles = (max_keys + 127) / 128;
-  const double most = blocks * Hkv * key_tiles;
-  const int pieces = most < sms ? (int)most : sms;
+  const double most = blocks * (Hkv / hg) * key_tiles;
+  const int pieces = most < sms / hg ? (int)most : sms / hg, ctas = pieces * hg;
   int box_rows = 16;
   while (box_rows < 128 && page_size % (2 * box_rows) == 0) box_rows *= 2;
   CUtensorMap m[5];
@@ -1143,6 +1154,8 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   p.win_r = win_r;
   p.sinks = sinks;
   p.pieces = pieces;
+  p.hg = hg;
+  p.ctas = ctas;
   p.block_table = block_table;
   p.seqlens = seqlens;
   p.cu = cu_seqlens;
@@ -1152,19 +1165,19 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   p.lse_part = reinterpret_cast<float*>(static_cast<char*>(ws) + wb.o_bytes);
   p.split = reinterpret_cast<int4*>(static_cast<char*>(ws) + wb.o_bytes + wb.lse_bytes);
   if (log_enabled())
-    std::fprintf(stderr, "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d few=%d pieces=%d box=%d win=(%d,%d) sinks=%d\n",
-                 B, total, Hq, Hkv, d, f8, tiles, few, pieces, box_rows, win_l, win_r, sinks);
+    std::fprintf(stderr, "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d few=%d pieces=%d hg=%d box=%d win=(%d,%d) sinks=%d\n",
+                 B, total, Hq, Hkv, d, f8, tiles, few, pieces, hg, box_rows, win_l, win_r, sinks);
   if (few) {
-    fa::fa_chunk_few_kernel<<<pieces, fa::kFewThreads, fa::FewCfg::kSmemBytes, cs>>>(
+    fa::fa_chunk_few_kernel<<<ctas, fa::kFewThreads, fa::FewCfg::kSmemBytes, cs>>>(
         m[1], m[2], m[3], m[4], static_cast<const __nv_bfloat16*>(q), q_stride, p);
     st = launch_status();
   } else {
-    st = d == 64 ? chunk_variant<64>(f8, tiles, pieces, m, p, cs) : chunk_variant<128>(f8, tiles, pieces, m, p, cs);
+    st = d == 64 ? chunk_variant<64>(f8, tiles, ctas, m, p, cs) : chunk_variant<128>(f8, tiles, ctas, m, p, cs);
   }
   // (with one key tile per block at most, or one piece, no block is spread over pieces)
   if (!st && pieces > 1 && key_tiles > 1)
-    st = d == 64 ? (tiles == 1 ? chunk_merge_launch<64, 1>(pieces, p, cs) : chunk_merge_launch<64, 2>(pieces, p, cs))
-                 : (tiles == 1 ? chunk_merge_launch<128, 1>(pieces, p, cs) : chunk_merge_launch<128, 2>(pieces, p, cs));
+    st = d == 64 ? (tiles == 1 ? chunk_merge_launch<64, 1>(ctas, p, cs) : chunk_merge_launch<64, 2>(ctas, p, cs))
+                 : (tiles == 1 ? chunk_merge_launch<128, 1>(ctas, p, cs) : chunk_merge_launch<128, 2>(ctas, p, cs));
   if (!workspace && cudaFreeAsync(ws, cs) != cudaSuccess && !st) st = FA_ERR_CUDA;
   return st;
 }

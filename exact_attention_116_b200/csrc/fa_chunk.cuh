@@ -13,10 +13,13 @@
 // work is kTiles such tiles that share every K/V load. Its keys are visited in 128-key tiles: the
 // sink tiles before the window, then the window's (all tiles without one).
 //
-// Work split: for each key/value head, the key tiles of all blocks are listed block after block;
-// the lists of all heads, one after another, are cut into P equal contiguous pieces, one per CTA
-// (one CTA per SM). So every CTA visits the same number of key tiles (within one), for decoding
-// steps, long prompts and mixtures alike. A block that lies in one piece is finished by its CTA;
+// Work split: for each group of hg heads, the key tiles of all blocks are listed block after block;
+// the lists of all groups, one after another, are cut into P equal contiguous pieces. A piece takes
+// hg CTAs, one for each head of the group, next to each other; in all one CTA per SM. So every CTA
+// visits the same number of key tiles (within one), for decoding steps, long prompts and mixtures
+// alike, and the heads' rows of a token, which lie side by side in a page, are read at about the
+// same time: DRAM and L2 serve 512 bytes and more at a stretch, not 128 or 256 (measured at
+// fa_chunk_few_kernel). A block that lies in one piece is finished by its CTA;
 // otherwise each of its pieces writes a partial (O / l, log2 l + m) and fa_chunk_merge_kernel joins
 // them by their log-sum-exp. (The CTA that finished a block last used to join it: one CTA reading
 // all partials of 64 rows took 60 us of a 178 us call, 32 query heads over 131072 keys.)
@@ -53,18 +56,21 @@ struct ChunkParams {
   int box_rows;    // rows of one page box: the largest power of two that divides page_size, <= 128
   int max_pages, num_pages;
   float scale_log2;  // scale * log2(e)
-  int win_l, win_r;  // -1 = unbounded; causal already folded into win_r = 0
+  int win_l, win_r;  // -1 = unbounded, else < 2^30, as positions; causal already folded into win_r = 0
   int sinks;         // first keys that stay visible left of the window
-  int pieces;        // P
+  int pieces;        // P: the pieces of a head group's list
+  int hg;            // heads of a group, on CTAs next to each other
+  int ctas;          // P * hg
   const int* block_table;  // (B, max_pages)
   const int* seqlens;      // (B)
   const int* cu;           // (B + 1)
   __nv_bfloat16* o;        // (total, Hq, d)
   float* lse;              // (Hq, total), natural log
-  float* o_part;           // (2 P, kTiles, d / 4, 128, 4) fp32: a warp's rows lie side by side
-  float* lse_part;         // (2 P, kTiles * 128), log2 domain
-  int4* split;             // (P) the block that starts in piece r and goes on: first packed row, tokens
-                           // (0: none), head, 2 * last piece + (slot of piece r is 2 r + 1)
+  float* o_part;           // (2 ctas, kTiles, d / 4, 128, 4) fp32: a warp's rows lie side by side
+  float* lse_part;         // (2 ctas, kTiles * 128), log2 domain
+  int4* split;             // (ctas) the block that starts in the CTA's piece and goes on: first packed row,
+                           // tokens (0: none), head, 2 * (pieces it goes on through) + (its first partial
+                           // is slot 2 cta + 1)
 };
 
 template <int D, bool kF8, int kTiles>
@@ -125,7 +131,7 @@ struct ChunkKeys {
 __device__ __forceinline__ ChunkKeys chunk_keys(const ChunkParams& p, int n, int pos0, int pos1) {
   ChunkKeys k;
   k.vis_lo = p.win_l >= 0 ? max(0, pos0 - p.win_l) : 0;
-  k.vis_hi = p.win_r >= 0 ? (int)min((long long)n - 1, (long long)pos1 + p.win_r) : n - 1;
+  k.vis_hi = p.win_r >= 0 ? min(n - 1, pos1 + p.win_r) : n - 1;
   k.ns = 0;
   k.lo = 0;
   k.cnt = 1;
@@ -208,7 +214,7 @@ struct ChunkWalk {
       do {
         if (++b == p.B) {
           b = 0;
-          ++h;
+          h += p.hg;
         }
         s = chunk_seq(p, b);
       } while (s.rows == 0);
@@ -221,7 +227,7 @@ struct ChunkWalk {
   }
 };
 
-// The list of all heads, T tiles, in pieces: the first T % pieces of them one tile longer.
+// The list of all head groups, T tiles, in pieces: the first T % pieces of them one tile longer.
 struct ChunkSplit {
   long long each, more;
   __device__ __forceinline__ ChunkSplit(long long T, int pieces) {
@@ -255,13 +261,13 @@ __device__ __forceinline__ void chunk_publish(const ChunkParams& p, Bars* bars, 
   for (w.begin(p, bars); w.valid() && !ab.raised(); w.next(p)) {
     put(w.block());
     if (!w.whole() && w.start >= w.u0) {
-      const long long T = bars->th * p.Hkv;
+      const long long T = bars->th * (p.Hkv / p.hg);
       const int last = ChunkSplit(T, (int)min((long long)p.pieces, T)).of(w.start + w.keys.cnt - 1);
-      split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * last + (w.start > w.u0 ? 1 : 0));
+      split = make_int4(w.s.c0 + w.i0, w.ntok, w.h, 2 * (last - (int)blockIdx.x / p.hg) + (w.start > w.u0 ? 1 : 0));
     }
   }
   if (!ab.raised()) put(ChunkBlock{});
-  if (dbg_range(ab, blockIdx.x, 1, p.pieces)) p.split[blockIdx.x] = split;
+  if (dbg_range(ab, blockIdx.x, 1, p.ctas)) p.split[blockIdx.x] = split;
 }
 // Block i of the piece (all lanes of a warp, or one thread); null: there is none, or the CTA gave up.
 template <class Bars>
@@ -370,8 +376,8 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, Bars* bars, int
     incl = plan_scan(tiles, bars->sums[2], tid, th);
   }
   const long long excl = incl - tiles;
-  const long long T = th * p.Hkv;
-  const int pe = (int)min((long long)p.pieces, T), r = blockIdx.x;
+  const long long T = th * (p.Hkv / p.hg);
+  const int pe = (int)min((long long)p.pieces, T), r = blockIdx.x / p.hg;
   long long u0 = T, u1 = T;
   if (r < pe && T > 0) {
     const ChunkSplit split(T, pe);
@@ -394,7 +400,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, Bars* bars, int
         at += cnt;
         return true;
       }
-      bars->first_h = h;
+      bars->first_h = h * p.hg + blockIdx.x % p.hg;
       bars->first_b = bb;
       bars->first_blk = kk;
       bars->first_seq = s;
@@ -731,7 +737,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       const int pos = pos_lo + tok_in_tile;
       const bool mine = row < rows;
       const int kmax = (!mine || pos < 0) ? -1
-                       : p.win_r >= 0     ? (int)min((long long)w.n - 1, (long long)pos + p.win_r)
+                       : p.win_r >= 0     ? min(w.n - 1, pos + p.win_r)
                                           : w.n - 1;
       const int kmin = p.win_l >= 0 ? max(0, pos - p.win_l) : 0;
       float m_run = -INFINITY, l_run = 0.0f, lr_run = 0.0f;
@@ -762,7 +768,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         for (int cc = 0; cc < kC; ++cc) x[cc] = __uint_as_float(r[cc >> 5][cc & 31]);
 
         const int k1 = key0 + 127, kbase = key0 + kC * half;
-        const bool all = pos_lo >= 0 && k1 < w.n && (p.win_r < 0 || k1 <= (long long)pos_lo + p.win_r) &&
+        const bool all = pos_lo >= 0 && k1 < w.n && (p.win_r < 0 || k1 <= pos_lo + p.win_r) &&
                          (p.win_l < 0 || key0 >= pos_hi - p.win_l || k1 < p.sinks);
         bool none = false;  // no score of this warp is visible
         if (!all) {
@@ -876,7 +882,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         const long long tok = (long long)w.c0 + t * p.tq + tok_in_tile;
         const int head = w.h * p.G + head_in_group;
         const long long ptile = (long long)w.slot * kTiles + t;
-        const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.pieces * kTiles * 128;
+        const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.ctas * kTiles * 128;
 #pragma unroll 1
         for (int cc = (D / 2) * half; cc < (D / 2) * (half + 1); cc += 32) {
           uint32_t o[32];
@@ -1000,7 +1006,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
 }
 
 // Joins the blocks that are spread over several pieces: CTA (r, y) takes the block that starts in
-// piece r and goes on, if there is one, and of it rows [8 y, 8 y + 8): a thread takes four columns of
+// CTA r's piece and goes on, if there is one, and of it rows [8 y, 8 y + 8): a thread takes four columns of
 // one row. A row's partials are weighted by 2^(their log-sum-exp - the largest), in piece order: the
 // same sum in every run. Bound by the latency of the partials, which lie in L2: kBatch of them, with
 // their log-sum-exps, are on their way at once (few rows are spread over many pieces, two tiles of
@@ -1014,8 +1020,8 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const Chu
   griddep_wait();  // the pieces have been written
   const int pf = blockIdx.x;
   const int4 s = __ldcg(p.split + pf);
-  const int m = (s.w >> 1) - pf + 1, first = blockIdx.y * kMergeRows, nrows = min(kMergeRows, s.y * p.G - first);
-  if (nrows <= 0 || !dbg_range(none, pf, m, p.pieces)) return;
+  const int m = (s.w >> 1) + 1, first = blockIdx.y * kMergeRows, nrows = min(kMergeRows, s.y * p.G - first);
+  if (nrows <= 0 || !dbg_range(none, pf, (m - 1) * p.hg + 1, p.ctas)) return;
   // a warp's threads: rows side by side (their number rounded up to a power of two), then columns
   const int shift = nrows <= 1 ? 0 : 32 - __clz(nrows - 1);
   for (int e = threadIdx.x; e < (D / 4) << shift; e += kMergeThreads) {
@@ -1032,7 +1038,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const Chu
         lse[i] = -INFINITY;
         o4[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (from + i >= m) continue;
-        const long long tile = (2LL * (pf + from + i) + (from + i == 0 ? (s.w & 1) : 0)) * kTiles + t;
+        const long long tile = (2LL * (pf + (from + i) * p.hg) + (from + i == 0 ? (s.w & 1) : 0)) * kTiles + t;
         lse[i] = __ldcg(p.lse_part + tile * 128 + srow);
         o4[i] = __ldcg(reinterpret_cast<const float4*>(p.o_part + tile * 128 * D) + c4 * 128 + srow);
       }

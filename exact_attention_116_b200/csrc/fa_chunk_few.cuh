@@ -32,6 +32,7 @@
 namespace fa {
 
 constexpr int kFewRows = 16, kFewTerms = 3, kFewSlots = 5;
+constexpr int kFewBufs = 4;        // tiles of scores and of weights in flight: two pairs
 constexpr int kFewThreads = 384;
 constexpr int kFewD = 128;
 constexpr float kFewGrow = 4.0f;   // log2: how far a score may exceed its row's reference
@@ -41,19 +42,19 @@ struct FewCfg {
   static constexpr int kSlotBytes = 128 * kFewD + 1024;  // codes, then the scales of each page box at 128 bytes
   static constexpr int kQBytes = kFewTerms * kFewRows * kFewD, kWBytes = kFewTerms * kFewRows * 128;
   static constexpr int kOffK = 0, kOffV = kFewSlots * kSlotBytes;
-  static constexpr int kOffQ = 2 * kFewSlots * kSlotBytes;  // two buffers each
+  static constexpr int kOffQ = 2 * kFewSlots * kSlotBytes;  // two buffers
   static constexpr int kOffW = kOffQ + 2 * kQBytes;
-  static constexpr int kOffX = kOffW + 2 * kWBytes;         // maxima and sums: [warp][row], three of them
+  static constexpr int kOffX = kOffW + kFewBufs * kWBytes;         // maxima and sums: [warp][row], three of them
   static constexpr int kOffBar = kOffX + 1024;
   static constexpr int kSmemBytes = kOffBar + 1536 + 1024;
-  static constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 128;  // S: two buffers of 16 columns
+  static constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 128;  // S: buffers of 16 columns
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
 struct FewBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[2][kFewSlots], empty[2][kFewSlots];  // K, V tiles
-  uint64_t s_full[2], s_empty[2], w_full[2], pv_done[2];
+  uint64_t s_full[kFewBufs], s_empty[kFewBufs], w_full[kFewBufs], pv_done[kFewBufs];
   uint64_t block_full[kBlockRing], block_empty[kBlockRing];
   uint64_t mma_done;
   uint32_t tmem_base;
@@ -138,8 +139,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (i < 2) count = 128;                                  // q_full: the splitting threads
       else if (i < 4) count = 5;                               // q_empty: the MMAs, the softmax warps
       else if (i >= kEmptyK && i < kEmptyK + kFewSlots) count = 5;  // K tile: the same (its scales)
-      else if (i >= kS + 2 && i < kS + 6) count = 4;           // s_empty, w_full: the softmax warps
-      else if (i >= kBars - 1 - kBlockRing && i < kBars - 1) count = 10;  // block_empty: loads, MMAs, softmax, queries
+      else if (i >= kS + kFewBufs && i < kS + 3 * kFewBufs) count = 4;           // s_empty, w_full: the softmax warps
+      else if (i >= kBars - 1 - kBlockRing && i < kBars - 1) count = 11;  // block_empty: loads, MMAs, softmax, queries
       if (i < kBars) mbar_init(first + i * 8, count);
     }
     fence_barrier_init();
@@ -165,13 +166,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   auto sT = [&](int kv, uint32_t slot) { return smem_base + (kv ? Cfg::kOffV : Cfg::kOffK) + slot * Cfg::kSlotBytes; };
   const int box_shift = 31 - __clz(p.box_rows);
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer (all lanes)
-    // Lane l < 16 loads the codes of page box l of a tile, lane 16 + l its scales; boxes of keys that
+  if (warp == 0 || warp == 2) {
+    // ---------------------------------------------------------------- TMA producers (all lanes): K and V
+    // (One warp took 1100 cycles to place and issue the four loads of a tile.) Lane l < 16 loads the codes of page box l of a tile, lane 16 + l its scales; boxes of keys that
     // no row sees are filled with zeros (page num_pages), as in fa_chunk_kernel.
     const int groups = 128 / p.box_rows, grp = lane & 15;
     const bool loads = grp < groups, scales = lane >= 16;
     const uint32_t box_off = (uint32_t)grp * p.box_rows;
+    const int kv = warp == 2 ? 1 : 0;
+    const CUtensorMap *tm = kv ? &tmV : &tmK, *tms = kv ? &tmVs : &tmKs;
     uint32_t n = 0;
     const ChunkBlock* block;
     for (uint32_t bi = 0; (block = chunk_take(bars, bi, ab)) && !ab.raised(); ++bi) {
@@ -201,35 +204,28 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         if (v + 1 < w.v1) place(v + 1, page, row);  // the next tile's page, read while this one waits
         const uint32_t slot = n % kFewSlots, phase = (n / kFewSlots) & 1;
-        bool ok = true;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          mbar_wait(bar(bars->empty[kv][slot]), phase ^ 1, ab);
-          const uint32_t to = sT(kv, slot) + box_off * D;
-          if (FA_DEBUG) {
-            ok = !loads || dbg_tma(ab, 0, w.h, rw, pg, D, p.Hkv, p.page_size, p.num_pages + 1, 1, to, p.box_rows * D,
-                                   smem_base, smem_end);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(bar(bars->full[kv][slot]), 128 * D + 128);
-          __syncwarp();
-          if (loads && !scales)
-            tma_load_4d(to, kv ? &tmV : &tmK, bar(bars->full[kv][slot]), 0, w.h, rw, pg);
-          else if (loads)
-            tma_load_2d(sT(kv, slot) + 128 * D + grp * 128, kv ? &tmVs : &tmKs, bar(bars->full[kv][slot]), rw,
-                        pg * p.Hkv + w.h);
+        mbar_wait(bar(bars->empty[kv][slot]), phase ^ 1, ab);
+        const uint32_t to = sT(kv, slot) + box_off * D;
+        if (FA_DEBUG) {
+          const bool ok = !loads || dbg_tma(ab, 0, w.h, rw, pg, D, p.Hkv, p.page_size, p.num_pages + 1, 1, to,
+                                            p.box_rows * D, smem_base, smem_end);
+          if (!__all_sync(0xffffffffu, ok)) break;
         }
-        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(bars->full[kv][slot]), 128 * D + 128);
+        __syncwarp();
+        if (loads && !scales)
+          tma_load_4d(to, tm, bar(bars->full[kv][slot]), 0, w.h, rw, pg);
+        else if (loads)
+          tma_load_2d(sT(kv, slot) + 128 * D + grp * 128, tms, bar(bars->full[kv][slot]), rw, pg * p.Hkv + w.h);
       }
       __syncwarp();
       if (lane == 0) chunk_release(bars, bi);
     }
     for (uint32_t i = n > kFewSlots ? n - kFewSlots : 0; i < n; ++i)  // every load issued lands before the CTA exits
-      for (int kv = 0; kv < 2; ++kv) mbar_drain(bar(bars->full[kv][i % kFewSlots]), (i / kFewSlots) & 1);
+      mbar_drain(bar(bars->full[kv][i % kFewSlots]), (i / kFewSlots) & 1);
   } else if (warp == 3) {
     if (lane == 0) chunk_publish<1>(p, bars, ab);
-  } else if (warp == 2) {
+    __syncwarp();
     if (blockIdx.x == 0)
       report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, lane, 32);
   } else if (warp == 1) {
@@ -239,9 +235,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       constexpr uint32_t idO = idesc_e4m3_e5m2(D, kFewTerms * kFewRows, true);   // V^T: columns are contiguous
       uint32_t n = 0, blocks = 0;
       auto issue_s = [&](uint32_t i, uint32_t qb, bool last) {
-        const uint32_t slot = i % kFewSlots, buf = i & 1;
+        const uint32_t slot = i % kFewSlots, buf = i % kFewBufs;
         mbar_wait(bar(bars->full[0][slot]), (i / kFewSlots) & 1, ab);
-        mbar_wait(bar(bars->s_empty[buf]), ((i >> 1) & 1) ^ 1, ab);
+        mbar_wait(bar(bars->s_empty[buf]), ((i / kFewBufs) & 1) ^ 1, ab);
         tc_fence_after_sync();
         const uint32_t k_smem = sT(0, slot), q_smem = smem_base + Cfg::kOffQ + qb * Cfg::kQBytes;
 #pragma unroll
@@ -261,12 +257,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const uint32_t qb = blocks & 1;
         mbar_wait(bar(bars->q_full[qb]), (blocks >> 1) & 1, ab);
         tc_fence_after_sync();
-        issue_s(n, qb, nv == 1);
+        for (int v = 0; v < min(nv, kFewBufs); ++v) issue_s(n + v, qb, v + 1 == nv);
         for (int v = 0; v < nv; ++v, ++n) {
-          if (v + 1 < nv) issue_s(n + 1, qb, v + 2 == nv);
-          const uint32_t slot = n % kFewSlots, buf = n & 1;
+          const uint32_t slot = n % kFewSlots, buf = n % kFewBufs;
           mbar_wait(bar(bars->full[1][slot]), (n / kFewSlots) & 1, ab);
-          mbar_wait(bar(bars->w_full[buf]), (n >> 1) & 1, ab);
+          mbar_wait(bar(bars->w_full[buf]), (n / kFewBufs) & 1, ab);
           tc_fence_after_sync();
           const uint32_t w_smem = smem_base + Cfg::kOffW + buf * Cfg::kWBytes;
 #pragma unroll
@@ -275,6 +270,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                       idO, v > 0 || kk > 0);
           mma_commit(bar(bars->pv_done[buf]));
           mma_commit(bar(bars->empty[1][slot]));
+          if (v + kFewBufs < nv) issue_s(n + kFewBufs, qb, v + kFewBufs + 1 == nv);
         }
         chunk_release(bars, blocks);
       }
@@ -291,7 +287,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const uint32_t w_at = (uint32_t)key_in;  // byte of this key in a row of W, before the swizzle
     uint32_t n = 0, blocks = 0;
     auto pv_wait = [&](uint32_t i) {     // W V of tile i has been added
-      mbar_wait(bar(bars->pv_done[i & 1]), (i >> 1) & 1, ab);
+      mbar_wait(bar(bars->pv_done[i % kFewBufs]), (i / kFewBufs) & 1, ab);
       tc_fence_after_sync();
     };
     for (;; ++blocks) {
@@ -300,6 +296,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const ChunkBlock& w = *block;
       const int nv = w.v1 - w.v0, rows = w.ntok * p.G, pairs = (rows + 1) >> 1;
       const int pos0 = w.pos0, pos1 = pos0 + w.ntok - 1, keys = w.n;
+      // keys [lo_all, hi_all] are seen by every row (bounds of the window fit 32 bits: fa_chunk_paged)
+      const int hi_all = p.win_r >= 0 ? min(keys - 1, pos0 + p.win_r) : keys - 1;
+      const int lo_all = p.win_l >= 0 ? pos1 - p.win_l : 0;
       const uint32_t qb = blocks & 1;
       float2 c2[kPairs], m2[kPairs], l2[kPairs], lr2[kPairs];
       mbar_wait(bar(bars->q_full[qb]), (blocks >> 1) & 1, ab);
@@ -314,76 +313,97 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       int E = -1000;
       uint32_t unset = (1u << rows) - 1u;  // rows that have seen no key: their reference is not one yet
 
-      for (int v = 0; v < nv; ++v, ++n) {
-        const uint32_t slot = n % kFewSlots, buf = n & 1;
-        const int key0 = w.keys.tile(w.v0 + v) * 128, key = key0 + key_in;
-        mbar_wait(bar(bars->full[0][slot]), (n / kFewSlots) & 1, ab);
-        const uint32_t ks = smem_gen[sT(0, slot) - smem_base + scale_at];
-        mbar_wait(bar(bars->s_full[buf]), (n >> 1) & 1, ab);
+      // Two tiles at a time: this thread has key key_in of each. (One at a time took 1900 cycles a tile,
+      // most of them the latencies of the chain from the scores to the weights.)
+      for (int v = 0; v < nv; v += 2) {
+        const int tiles = min(2, nv - v);
+        float2 a[2][kPairs];
+        uint32_t vs[2];
+        bool seen[2] = {false, false};
+        float most = -INFINITY;
+        int ev = -1000;
+        // all waits first (the scores of the later tile imply the earlier one's), then all loads
+        uint32_t ks[2] = {0u, 0u}, r0[2][8] = {}, r1[2][8] = {};
+        mbar_wait(bar(bars->s_full[(n + tiles - 1) % kFewBufs]), ((n + tiles - 1) / kFewBufs) & 1, ab);
         tc_fence_after_sync();
-        float2 a[kPairs];
-        {
-          uint32_t r0[8], r1[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-          tmem_ld8(tmem + lane_field + Cfg::kColS + buf * kFewRows, r0);
-          if (pairs > 4) tmem_ld8(tmem + lane_field + Cfg::kColS + buf * kFewRows + 8, r1);
-          tmem_wait_ld(r0);
-          tmem_wait_ld(r1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a[i] = make_float2(__uint_as_float(r0[2 * i]), __uint_as_float(r0[2 * i + 1]));
-            a[i + 4] = make_float2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1]));
+        for (int u = 0; u < 2; ++u) {
+          if (u >= tiles) break;
+          const uint32_t at = tmem + lane_field + Cfg::kColS + (n + u) % kFewBufs * kFewRows;
+          tmem_ld8(at, r0[u]);
+          if (pairs > 4) tmem_ld8(at + 8, r1[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (u >= tiles) break;
+          const uint32_t i = n + u, slot = i % kFewSlots, buf = i % kFewBufs;
+          mbar_wait(bar(bars->full[0][slot]), (i / kFewSlots) & 1, ab);
+          ks[u] = smem_gen[sT(0, slot) - smem_base + scale_at];
+          mbar_wait(bar(bars->full[1][slot]), (i / kFewSlots) & 1, ab);
+          vs[u] = smem_gen[sT(1, slot) - smem_base + scale_at];
+          if (i >= kFewBufs) mbar_wait(bar(bars->pv_done[buf]), ((i / kFewBufs) & 1) ^ 1, ab);  // W has been read
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          tmem_wait_ld(r0[u]);
+          tmem_wait_ld(r1[u]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            a[u][k] = make_float2(__uint_as_float(r0[u][2 * k]), __uint_as_float(r0[u][2 * k + 1]));
+            a[u][k + 4] = make_float2(__uint_as_float(r1[u][2 * k]), __uint_as_float(r1[u][2 * k + 1]));
           }
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(bars->s_empty[buf]));
-          mbar_arrive(bar(bars->empty[0][slot]));
+        if (lane < tiles) {
+          mbar_arrive(bar(bars->s_empty[(n + lane) % kFewBufs]));
+          mbar_arrive(bar(bars->empty[0][(n + lane) % kFewSlots]));
         }
-        mbar_wait(bar(bars->full[1][slot]), (n / kFewSlots) & 1, ab);
-        const uint32_t vs = smem_gen[sT(1, slot) - smem_base + scale_at];
-        const float kf = ks == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float((int)max(ks, 1u) << 23);
-
-        // scores against the references, -inf where masked; is the key seen at all?
-        const bool all = pos0 >= 0 && key0 + 127 < keys &&
-                         (p.win_r < 0 || key0 + 127 <= (long long)pos0 + p.win_r) &&
-                         (p.win_l < 0 || key0 >= pos1 - p.win_l || key0 + 127 < p.sinks);
-        bool seen = true;
-        float most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          if (i >= pairs) break;
-          a[i] = fma2(mul2(a[i], c2[i]), make_float2(kf, kf), make_float2(-m2[i].x, -m2[i].y));
-        }
-        if (!all) {
-          seen = false;
+        for (int u = 0; u < 2; ++u) {
+          if (u >= tiles) break;
+          const float kf = ks[u] == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000)
+                                                        : __int_as_float((int)max(ks[u], 1u) << 23);
+          // scores against the references, -inf where masked; is the key seen at all?
+          const int key0 = w.keys.tile(w.v0 + v + u) * 128, key = key0 + key_in;
+          const bool all = pos0 >= 0 && key0 + 127 <= hi_all && (key0 >= lo_all || key0 + 127 < p.sinks);
+          seen[u] = all;
 #pragma unroll
-          for (int i = 0; i < kPairs; ++i) {
-            if (i >= pairs) break;
+          for (int k = 0; k < kPairs; ++k) {
+            if (k >= pairs) break;
+            a[u][k] = fma2(mul2(a[u][k], c2[k]), make_float2(kf, kf), make_float2(-m2[k].x, -m2[k].y));
+          }
+          if (!all) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int pos = pos0 + p.by_group(2 * i + e);
-              const bool vis = pos >= 0 && key < keys && (p.win_r < 0 || key <= (long long)pos + p.win_r) &&
-                               (p.win_l < 0 || key >= pos - p.win_l || key < p.sinks) && 2 * i + e < rows;
-              seen |= vis;
-              if (!vis) (e ? a[i].y : a[i].x) = -INFINITY;
+            for (int k = 0; k < kPairs; ++k) {
+              if (k >= pairs) break;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int pos = pos0 + p.by_group(2 * k + e);
+                const bool vis = pos >= 0 && key < keys && (p.win_r < 0 || key <= pos + p.win_r) &&
+                                 (p.win_l < 0 || key >= pos - p.win_l || key < p.sinks) && 2 * k + e < rows;
+                seen[u] |= vis;
+                if (!vis) (e ? a[u][k].y : a[u][k].x) = -INFINITY;
+              }
             }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          if (i >= pairs) break;
-          most = max3(most, a[i].x, a[i].y);
+          for (int k = 0; k < kPairs; ++k) {
+            if (k >= pairs) break;
+            most = max3(most, a[u][k].x, a[u][k].y);
+          }
+          if (seen[u] && vs[u] != (uint32_t)kScaleNan) ev = max(ev, (int)vs[u] - 127);
         }
-        const int ev = seen && vs != (uint32_t)kScaleNan ? (int)vs - 127 : -1000;
         if (few_vote(most > kFewGrow || ev > E + 1 || unset != 0)) {
-          // exact maxima over the tile's keys; the sums and O follow the new references
+          // exact maxima over the tiles' keys; the sums and O follow the new references
           int em = __reduce_max_sync(0xffffffffu, ev);
 #pragma unroll
-          for (int i = 0; i < kPairs; ++i) {
-            if (i >= pairs) break;
-            const float x = warp_max_f32(a[i].x), y = warp_max_f32(a[i].y);
-            if (lane == 0) *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * i]) = make_float2(x, y);
+          for (int k = 0; k < kPairs; ++k) {
+            if (k >= pairs) break;
+            float2 x = a[0][k];
+            if (tiles > 1) x = make_float2(fmaxf(x.x, a[1][k].x), fmaxf(x.y, a[1][k].y));
+            x = make_float2(warp_max_f32(x.x), warp_max_f32(x.y));
+            if (lane == 0) *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * k]) = x;
           }
           if (lane == 0) sE[wq] = em;
           named_bar_sync(2, 128);
@@ -392,13 +412,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const float e_step = E <= -1000 ? 0.0f : exp2_int(E - e_new);
           float2 alpha[kPairs];
 #pragma unroll
-          for (int i = 0; i < kPairs; ++i) {
-            alpha[i] = make_float2(1.0f, 1.0f);
-            if (i >= pairs) continue;
+          for (int k = 0; k < kPairs; ++k) {
+            alpha[k] = make_float2(1.0f, 1.0f);
+            if (k >= pairs) continue;
             float2 x = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float2 y = *reinterpret_cast<const float2*>(&sX[u * kFewRows + 2 * i]);
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const float2 y = *reinterpret_cast<const float2*>(&sX[q4 * kFewRows + 2 * k]);
               x = make_float2(fmaxf(x.x, y.x), fmaxf(x.y, y.y));
             }
             float2 up;  // rise of the references; a first one may lie anywhere
@@ -408,12 +428,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               alpha_r = first ? 1.0f : ex2_approx(-up_r);
               if (most_r != -INFINITY) unset &= ~(1u << r);
             };
-            rise(x.x, 2 * i, up.x, alpha[i].x);
-            rise(x.y, 2 * i + 1, up.y, alpha[i].y);
-            m2[i] = add2(m2[i], up);
-            a[i] = sub2(a[i], up);
-            l2[i] = mul2(l2[i], alpha[i]);
-            lr2[i] = mul2(lr2[i], alpha[i]);
+            rise(x.x, 2 * k, up.x, alpha[k].x);
+            rise(x.y, 2 * k + 1, up.y, alpha[k].y);
+            m2[k] = add2(m2[k], up);
+            a[0][k] = sub2(a[0][k], up);
+            a[1][k] = sub2(a[1][k], up);
+            l2[k] = mul2(l2[k], alpha[k]);
+            lr2[k] = mul2(lr2[k], alpha[k]);
           }
           E = e_new;
           if (v > 0) {
@@ -428,9 +449,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 tmem_ld8(at, o);
                 tmem_wait_ld(o);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) * (alpha[hf * 4 + i].x * e_step));
-                  o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) * (alpha[hf * 4 + i].y * e_step));
+                for (int k = 0; k < 4; ++k) {
+                  o[2 * k] = __float_as_uint(__uint_as_float(o[2 * k]) * (alpha[hf * 4 + k].x * e_step));
+                  o[2 * k + 1] = __float_as_uint(__uint_as_float(o[2 * k + 1]) * (alpha[hf * 4 + k].y * e_step));
                 }
                 tmem_st8(at, o);
               }
@@ -438,37 +459,42 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
           named_bar_sync(2, 128);  // sX and sE have been read
         }
-        const float vf = vs == (uint32_t)kScaleNan && seen ? __int_as_float(0x7fc00000)
-                         : seen                          ? exp2_int((int)vs - 127 - E + kFewShift)
-                                                         : 0.0f;
-        if (n >= 2) mbar_wait(bar(bars->pv_done[buf]), ((n >> 1) & 1) ^ 1, ab);  // tile n - 2 has read this W buffer
-        const uint32_t w_smem = smem_base + Cfg::kOffW + buf * Cfg::kWBytes;
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          if (i >= pairs) break;
-          const float2 pe = make_float2(ex2_approx(a[i].x), ex2_approx(a[i].y));
-          l2[i] = add2(l2[i], pe);
-          const float2 pr = round_bits2<9>(pe);
-          lr2[i] = add2(lr2[i], pr);
-          uint32_t t[kFewTerms];
-          split_e5m2(mul2(pr, make_float2(vf, vf)), t);
+        for (int u = 0; u < 2; ++u) {
+          if (u >= tiles) break;
+          const uint32_t i = n + u, slot = i % kFewSlots, buf = i % kFewBufs;
+          const float vf = !seen[u]                        ? 0.0f
+                           : vs[u] == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000)
+                                                          : exp2_int((int)vs[u] - 127 - E + kFewShift);
+          const uint32_t w_smem = smem_base + Cfg::kOffW + buf * Cfg::kWBytes;
 #pragma unroll
-          for (int term = 0; term < kFewTerms; ++term) {
+          for (int k = 0; k < kPairs; ++k) {
+            if (k >= pairs) break;
+            const float2 pe = make_float2(ex2_approx(a[u][k].x), ex2_approx(a[u][k].y));
+            l2[k] = add2(l2[k], pe);
+            const float2 pr = round_bits2<9>(pe);
+            lr2[k] = add2(lr2[k], pr);
+            uint32_t t[kFewTerms];
+            split_e5m2(mul2(pr, make_float2(vf, vf)), t);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = term * kFewRows + 2 * i + e;
-              st_shared_u8(w_smem + r * 128 + (w_at ^ ((r & 7) << 4)), e ? t[term] >> 8 : t[term]);
+            for (int term = 0; term < kFewTerms; ++term) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int r = term * kFewRows + 2 * k + e;
+                st_shared_u8(w_smem + r * 128 + (w_at ^ ((r & 7) << 4)), e ? t[term] >> 8 : t[term]);
+              }
             }
           }
-        }
-        if (!seen) {  // the row of a key that no row sees may hold anything: 0 (its weights are 0)
+          if (!seen[u]) {  // the row of a key that no row sees may hold anything: 0 (its weights are 0)
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) st_shared_v4(sT(1, slot) + key_in * D + i * 16, 0u, 0u, 0u, 0u);
+            for (int k = 0; k < D / 16; ++k) st_shared_v4(sT(1, slot) + key_in * D + k * 16, 0u, 0u, 0u, 0u);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars->w_full[buf]));
+        if (lane < tiles) mbar_arrive(bar(bars->w_full[(n + lane) % kFewBufs]));
+        n += tiles;
       }
 
       // ---- epilogue: this thread's column of every row
@@ -490,7 +516,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       named_bar_sync(2, 128);
       if (nv > 0) pv_wait(n - 1);
       const float e_unit = exp2_int(max(E, -110) - kFewShift);
-      const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.pieces * 128;
+      const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.ctas * 128;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         if (hf * 8 >= rows) break;

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
                         const __nv_bfloat16* __restrict__ q, long long q_stride, const ChunkParams p) {
   using Cfg = FewCfg;
-  constexpr int D = kFewD, kPairs = kFewRows / 2;
+  constexpr int D = kFewD;
   static_assert(sizeof(FewBars) <= 1536, "barrier block");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -290,23 +290,22 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       mbar_wait(bar(bars->pv_done[i % kFewBufs]), (i / kFewBufs) & 1, ab);
       tc_fence_after_sync();
     };
-    for (;; ++blocks) {
-      const ChunkBlock* block = chunk_take(bars, blocks, ab);
-      if (!all_agree(block != nullptr, 2, 128)) break;  // (the warps meet at this barrier: all go on, or none)
-      const ChunkBlock& w = *block;
-      const int nv = w.v1 - w.v0, rows = w.ntok * p.G, pairs = (rows + 1) >> 1;
+    // One block of at most 2 kPairs rows.
+    auto block_rows = [&](auto np, const ChunkBlock& w) {
+      constexpr int kPairs = decltype(np)::value;
+      const int nv = w.v1 - w.v0, rows = w.ntok * p.G, v0 = w.v0;
       const int pos0 = w.pos0, pos1 = pos0 + w.ntok - 1, keys = w.n;
+      const int tile_ns = w.keys.ns, tile_lo = w.keys.lo;
       // keys [lo_all, hi_all] are seen by every row (bounds of the window fit 32 bits: fa_chunk_paged)
-      const int hi_all = p.win_r >= 0 ? min(keys - 1, pos0 + p.win_r) : keys - 1;
+      const int hi_all = pos0 < 0 ? -1 : p.win_r >= 0 ? min(keys - 1, pos0 + p.win_r) : keys - 1;
       const int lo_all = p.win_l >= 0 ? pos1 - p.win_l : 0;
       const uint32_t qb = blocks & 1;
       float2 c2[kPairs], m2[kPairs], l2[kPairs], lr2[kPairs];
       mbar_wait(bar(bars->q_full[qb]), (blocks >> 1) & 1, ab);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        c2[i] = *reinterpret_cast<const float2*>(&bars->q_factor[qb][2 * i]);
-        m2[i] = make_float2(0.0f, 0.0f);
-        l2[i] = lr2[i] = make_float2(0.0f, 0.0f);
+      for (int k = 0; k < kPairs; ++k) {
+        c2[k] = *reinterpret_cast<const float2*>(&bars->q_factor[qb][2 * k]);
+        m2[k] = l2[k] = lr2[k] = make_float2(0.0f, 0.0f);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars->q_empty[qb]));
@@ -316,82 +315,86 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // Two tiles at a time: this thread has key key_in of each. (One at a time took 1900 cycles a tile,
       // most of them the latencies of the chain from the scores to the weights.)
       for (int v = 0; v < nv; v += 2) {
-        const int tiles = min(2, nv - v);
-        float2 a[2][kPairs];
-        uint32_t vs[2];
-        bool seen[2] = {false, false};
-        float most = -INFINITY;
-        int ev = -1000;
-        // all waits first (the scores of the later tile imply the earlier one's), then all loads
-        uint32_t ks[2] = {0u, 0u}, r0[2][8] = {}, r1[2][8] = {};
-        mbar_wait(bar(bars->s_full[(n + tiles - 1) % kFewBufs]), ((n + tiles - 1) / kFewBufs) & 1, ab);
-        tc_fence_after_sync();
+        const bool two = v + 1 < nv;
+        const uint32_t n1 = n + (two ? 1 : 0);  // the last of the tiles
+        uint32_t slot[2], buf[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (u >= tiles) break;
-          const uint32_t at = tmem + lane_field + Cfg::kColS + (n + u) % kFewBufs * kFewRows;
-          tmem_ld8(at, r0[u]);
-          if (pairs > 4) tmem_ld8(at + 8, r1[u]);
+          slot[u] = (u ? n1 : n) % kFewSlots;
+          buf[u] = (u ? n1 : n) % kFewBufs;
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (u >= tiles) break;
-          const uint32_t i = n + u, slot = i % kFewSlots, buf = i % kFewBufs;
-          mbar_wait(bar(bars->full[0][slot]), (i / kFewSlots) & 1, ab);
-          ks[u] = smem_gen[sT(0, slot) - smem_base + scale_at];
-          mbar_wait(bar(bars->full[1][slot]), (i / kFewSlots) & 1, ab);
-          vs[u] = smem_gen[sT(1, slot) - smem_base + scale_at];
-          if (i >= kFewBufs) mbar_wait(bar(bars->pv_done[buf]), ((i / kFewBufs) & 1) ^ 1, ab);  // W has been read
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          tmem_wait_ld(r0[u]);
-          tmem_wait_ld(r1[u]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[u][k] = make_float2(__uint_as_float(r0[u][2 * k]), __uint_as_float(r0[u][2 * k + 1]));
-            a[u][k + 4] = make_float2(__uint_as_float(r1[u][2 * k]), __uint_as_float(r1[u][2 * k + 1]));
+        {
+          // the waits of this step, a lane each: scores (the later tile's come last), K and V (for their
+          // scales), and that the weights' buffers have been read (the same)
+          const uint32_t i = lane == 1 || lane == 3 ? n : n1;
+          const uint32_t k_bar = bar(bars->full[0][i % kFewSlots]), v_bar = bar(bars->full[1][i % kFewSlots]);
+          uint32_t at = bar(bars->s_full[buf[1]]), parity = (n1 / kFewBufs) & 1;
+          if (lane >= 1 && lane < 5) {
+            at = lane < 3 ? k_bar : v_bar;
+            parity = (i / kFewSlots) & 1;
+          } else if (lane == 5 && n1 >= kFewBufs) {
+            at = bar(bars->pv_done[buf[1]]);
+            parity ^= 1;
           }
+          mbar_wait(at, parity, ab);
+          __syncwarp();
         }
+        tc_fence_after_sync();
+        constexpr int kHalves = kPairs > 4 ? 2 : 1;
+        uint32_t r[2][kHalves][8], ks[2], vs[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int hf = 0; hf < kHalves; ++hf)
+            tmem_ld8(tmem + lane_field + Cfg::kColS + buf[u] * kFewRows + hf * 8, r[u][hf]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          ks[u] = smem_gen[sT(0, slot[u]) - smem_base + scale_at];
+          vs[u] = smem_gen[sT(1, slot[u]) - smem_base + scale_at];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int hf = 0; hf < kHalves; ++hf) tmem_wait_ld(r[u][hf]);
         tc_fence_before_sync();
         __syncwarp();
-        if (lane < tiles) {
+        if (lane < (two ? 2 : 1)) {
           mbar_arrive(bar(bars->s_empty[(n + lane) % kFewBufs]));
           mbar_arrive(bar(bars->empty[0][(n + lane) % kFewSlots]));
         }
+
+        // scores against the references, -inf where masked; is the key seen at all?
+        float2 a[2][kPairs];
+        bool seen[2];
+        float most = -INFINITY;
+        int ev = -1000;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (u >= tiles) break;
           const float kf = ks[u] == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000)
                                                         : __int_as_float((int)max(ks[u], 1u) << 23);
-          // scores against the references, -inf where masked; is the key seen at all?
-          const int key0 = w.keys.tile(w.v0 + v + u) * 128, key = key0 + key_in;
-          const bool all = pos0 >= 0 && key0 + 127 <= hi_all && (key0 >= lo_all || key0 + 127 < p.sinks);
-          seen[u] = all;
+          const int tile = v0 + v + u, key0 = (tile < tile_ns ? tile : tile_lo + tile - tile_ns) * 128, key = key0 + key_in;
+          const bool on = u == 0 || two, all = key0 + 127 <= hi_all && (key0 >= lo_all || key0 + 127 < p.sinks);
+          seen[u] = on && all;
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) {
-            if (k >= pairs) break;
-            a[u][k] = fma2(mul2(a[u][k], c2[k]), make_float2(kf, kf), make_float2(-m2[k].x, -m2[k].y));
+            const float2 x = make_float2(__uint_as_float(r[u][k / 4][2 * (k % 4)]),
+                                         __uint_as_float(r[u][k / 4][2 * (k % 4) + 1]));
+            a[u][k] = fma2(mul2(x, c2[k]), make_float2(kf, kf), make_float2(-m2[k].x, -m2[k].y));
           }
-          if (!all) {
+          if (!(on && all)) {
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) {
-              if (k >= pairs) break;
+            for (int k = 0; k < kPairs; ++k)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int pos = pos0 + p.by_group(2 * k + e);
-                const bool vis = pos >= 0 && key < keys && (p.win_r < 0 || key <= pos + p.win_r) &&
+                const bool vis = on && pos >= 0 && key < keys && (p.win_r < 0 || key <= pos + p.win_r) &&
                                  (p.win_l < 0 || key >= pos - p.win_l || key < p.sinks) && 2 * k + e < rows;
                 seen[u] |= vis;
                 if (!vis) (e ? a[u][k].y : a[u][k].x) = -INFINITY;
               }
-            }
           }
 #pragma unroll
-          for (int k = 0; k < kPairs; ++k) {
-            if (k >= pairs) break;
-            most = max3(most, a[u][k].x, a[u][k].y);
-          }
+          for (int k = 0; k < kPairs; ++k) most = max3(most, a[u][k].x, a[u][k].y);
           if (seen[u] && vs[u] != (uint32_t)kScaleNan) ev = max(ev, (int)vs[u] - 127);
         }
         if (few_vote(most > kFewGrow || ev > E + 1 || unset != 0)) {
@@ -399,10 +402,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           int em = __reduce_max_sync(0xffffffffu, ev);
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) {
-            if (k >= pairs) break;
-            float2 x = a[0][k];
-            if (tiles > 1) x = make_float2(fmaxf(x.x, a[1][k].x), fmaxf(x.y, a[1][k].y));
-            x = make_float2(warp_max_f32(x.x), warp_max_f32(x.y));
+            const float2 x = make_float2(warp_max_f32(fmaxf(a[0][k].x, a[1][k].x)), warp_max_f32(fmaxf(a[0][k].y, a[1][k].y)));
             if (lane == 0) *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * k]) = x;
           }
           if (lane == 0) sE[wq] = em;
@@ -413,8 +413,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           float2 alpha[kPairs];
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) {
-            alpha[k] = make_float2(1.0f, 1.0f);
-            if (k >= pairs) continue;
             float2 x = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
@@ -422,11 +420,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               x = make_float2(fmaxf(x.x, y.x), fmaxf(x.y, y.y));
             }
             float2 up;  // rise of the references; a first one may lie anywhere
-            auto rise = [&](float most_r, int r, float& up_r, float& alpha_r) {
-              const bool first = (unset >> r) & 1;
+            auto rise = [&](float most_r, int row, float& up_r, float& alpha_r) {
+              const bool first = (unset >> row) & 1;
               up_r = first ? (most_r == -INFINITY ? 0.0f : most_r) : fmaxf(most_r, 0.0f);
               alpha_r = first ? 1.0f : ex2_approx(-up_r);
-              if (most_r != -INFINITY) unset &= ~(1u << r);
+              if (most_r != -INFINITY) unset &= ~(1u << row);
             };
             rise(x.x, 2 * k, up.x, alpha[k].x);
             rise(x.y, 2 * k + 1, up.y, alpha[k].y);
@@ -442,14 +440,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
             for (int term = 0; term < kFewTerms; ++term)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                if (hf * 4 >= pairs) continue;
+              for (int hf = 0; hf < kHalves; ++hf) {
                 uint32_t o[8];
                 const uint32_t at = tmem + lane_field + Cfg::kColO + term * kFewRows + hf * 8;
                 tmem_ld8(at, o);
                 tmem_wait_ld(o);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
+                  if (hf * 4 + k >= kPairs) continue;
                   o[2 * k] = __float_as_uint(__uint_as_float(o[2 * k]) * (alpha[hf * 4 + k].x * e_step));
                   o[2 * k + 1] = __float_as_uint(__uint_as_float(o[2 * k + 1]) * (alpha[hf * 4 + k].y * e_step));
                 }
@@ -459,91 +457,96 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
           named_bar_sync(2, 128);  // sX and sE have been read
         }
+        // weights: rounded, summed, and in three terms into their buffers
+        float vf[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (u >= tiles) break;
-          const uint32_t i = n + u, slot = i % kFewSlots, buf = i % kFewBufs;
-          const float vf = !seen[u]                        ? 0.0f
-                           : vs[u] == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000)
-                                                          : exp2_int((int)vs[u] - 127 - E + kFewShift);
-          const uint32_t w_smem = smem_base + Cfg::kOffW + buf * Cfg::kWBytes;
+        for (int u = 0; u < 2; ++u)
+          vf[u] = !seen[u]                        ? 0.0f
+                  : vs[u] == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000)
+                                                 : exp2_int((int)vs[u] - 127 - E + kFewShift);
 #pragma unroll
-          for (int k = 0; k < kPairs; ++k) {
-            if (k >= pairs) break;
+        for (int k = 0; k < kPairs; ++k) {
+          uint32_t t[2][kFewTerms];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
             const float2 pe = make_float2(ex2_approx(a[u][k].x), ex2_approx(a[u][k].y));
             l2[k] = add2(l2[k], pe);
             const float2 pr = round_bits2<9>(pe);
             lr2[k] = add2(lr2[k], pr);
-            uint32_t t[kFewTerms];
-            split_e5m2(mul2(pr, make_float2(vf, vf)), t);
+            split_e5m2(mul2(pr, make_float2(vf[u], vf[u])), t[u]);
+          }
 #pragma unroll
-            for (int term = 0; term < kFewTerms; ++term) {
+          for (int u = 0; u < 2; ++u) {
+            if (u == 1 && !two) continue;  // (the buffer is not this block's)
+            const uint32_t w_smem = smem_base + Cfg::kOffW + buf[u] * Cfg::kWBytes;
+#pragma unroll
+            for (int term = 0; term < kFewTerms; ++term)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int r = term * kFewRows + 2 * k + e;
-                st_shared_u8(w_smem + r * 128 + (w_at ^ ((r & 7) << 4)), e ? t[term] >> 8 : t[term]);
+                const int row = term * kFewRows + 2 * k + e;
+                st_shared_u8(w_smem + row * 128 + (w_at ^ ((row & 7) << 4)), e ? t[u][term] >> 8 : t[u][term]);
               }
-            }
-          }
-          if (!seen[u]) {  // the row of a key that no row sees may hold anything: 0 (its weights are 0)
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) st_shared_v4(sT(1, slot) + key_in * D + k * 16, 0u, 0u, 0u, 0u);
           }
         }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (!seen[u] && (u == 0 || two)) {  // the row of a key that no row sees may hold anything: 0
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) st_shared_v4(sT(1, slot[u]) + key_in * D + k * 16, 0u, 0u, 0u, 0u);
+          }
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane < tiles) mbar_arrive(bar(bars->w_full[(n + lane) % kFewBufs]));
-        n += tiles;
+        if (lane < (two ? 2 : 1)) mbar_arrive(bar(bars->w_full[(n + lane) % kFewBufs]));
+        n = n1 + 1;
       }
 
       // ---- epilogue: this thread's column of every row
       const bool whole = w.slot < 0;
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        if (i >= pairs) break;
-        float2 a = l2[i], b = lr2[i];
+      for (int k = 0; k < kPairs; ++k) {
+        float2 a = l2[k], b = lr2[k];
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
           a = add2(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, off), __shfl_xor_sync(0xffffffffu, a.y, off)));
           b = add2(b, make_float2(__shfl_xor_sync(0xffffffffu, b.x, off), __shfl_xor_sync(0xffffffffu, b.y, off)));
         }
         if (lane == 0) {
-          *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * i]) = a;
-          *reinterpret_cast<float2*>(&sX[(4 + wq) * kFewRows + 2 * i]) = b;
+          *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * k]) = a;
+          *reinterpret_cast<float2*>(&sX[(4 + wq) * kFewRows + 2 * k]) = b;
         }
       }
       named_bar_sync(2, 128);
-      if (nv > 0) pv_wait(n - 1);
+      pv_wait(n - 1);
       const float e_unit = exp2_int(max(E, -110) - kFewShift);
       const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.ctas * 128;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (hf * 8 >= rows) break;
+      for (int hf = 0; hf < (kPairs > 4 ? 2 : 1); ++hf) {
         float o[8];
 #pragma unroll
         for (int term = 0; term < kFewTerms; ++term) {
-          uint32_t r[8];
-          tmem_ld8(tmem + lane_field + Cfg::kColO + term * kFewRows + hf * 8, r);
-          tmem_wait_ld(r);
+          uint32_t x[8];
+          tmem_ld8(tmem + lane_field + Cfg::kColO + term * kFewRows + hf * 8, x);
+          tmem_wait_ld(x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = term == 0 ? __uint_as_float(r[i]) : o[i] + __uint_as_float(r[i]);
+          for (int i = 0; i < 8; ++i) o[i] = term == 0 ? __uint_as_float(x[i]) : o[i] + __uint_as_float(x[i]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = hf * 8 + i;
-          if (r >= rows) break;
+          constexpr int kLast = 2 * kPairs;
+          const int row = hf * 8 + i;
+          if (row >= kLast || row >= rows) break;
           float l = 0.0f, lr = 0.0f;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            l += sX[u * kFewRows + r];
-            lr += sX[(4 + u) * kFewRows + r];
+            l += sX[u * kFewRows + row];
+            lr += sX[(4 + u) * kFewRows + row];
           }
           const bool dead = !(lr > 0.0f) && lr == lr;  // no visible key (a NaN sum is not one)
           const float value = dead ? 0.0f : o[i] * e_unit / lr;
-          const float m = (i & 1) ? m2[r >> 1].y : m2[r >> 1].x;
+          const float m = (row & 1) ? m2[row < kLast ? row >> 1 : 0].y : m2[row < kLast ? row >> 1 : 0].x;
           const float lse2 = l > 0.0f ? m + lg2_approx(l) : (l == l ? -INFINITY : l);
-          const int itok = p.by_group(r), head = w.h * p.G + r - itok * p.G;
+          const int itok = p.by_group(row), head = w.h * p.G + row - itok * p.G;
           const long long tok = (long long)w.c0 + itok;
           if (whole) {
             const long long oi = (tok * p.Hq + head) * D + key_in, li = (long long)head * p.total + tok;
@@ -552,15 +555,31 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               p.lse[li] = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
           } else {
             const long long pi = (long long)w.slot * 128;
-            if (dbg_range(ab, pi + r, 1, part_rows)) {
-              p.o_part[pi * D + ((key_in >> 2) * 128 + r) * 4 + (key_in & 3)] = value;
-              if (key_in == 0) p.lse_part[pi + r] = lse2;
+            if (dbg_range(ab, pi + row, 1, part_rows)) {
+              p.o_part[pi * D + ((key_in >> 2) * 128 + row) * 4 + (key_in & 3)] = value;
+              if (key_in == 0) p.lse_part[pi + row] = lse2;
             }
           }
         }
       }
       tc_fence_before_sync();
       named_bar_sync(2, 128);  // the sums have been read
+    };
+    for (;; ++blocks) {
+      const ChunkBlock* block = chunk_take(bars, blocks, ab);
+      if (!all_agree(block != nullptr, 2, 128)) break;  // (the warps meet at this barrier: all go on, or none)
+      const ChunkBlock& w = *block;
+      const int rows = w.ntok * p.G;
+      // (straight-line code for the number of row pairs: a branch per pair kept the chains of different
+      // pairs and tiles from overlapping)
+      if (rows <= 2)
+        block_rows(std::integral_constant<int, 1>(), w);
+      else if (rows <= 4)
+        block_rows(std::integral_constant<int, 2>(), w);
+      else if (rows <= 8)
+        block_rows(std::integral_constant<int, 4>(), w);
+      else
+        block_rows(std::integral_constant<int, 8>(), w);
       if (lane == 0) chunk_release(bars, blocks);
     }
   } else if (warp >= 8) {

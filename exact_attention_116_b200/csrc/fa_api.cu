@@ -576,7 +576,7 @@ int launch_cache(const fa::CacheParams& p, int d, cudaStream_t stream) {
   else
     kernel = d == 64 ? (f8 ? fa::fa_cache_read_kernel<64, true> : fa::fa_cache_read_kernel<64, false>)
                      : (f8 ? fa::fa_cache_read_kernel<128, true> : fa::fa_cache_read_kernel<128, false>);
-  kernel<<<(unsigned)blocks, fa::kCacheThreads, 0, stream>>>(p);
+  kernel<<<dim3((unsigned)blocks, 2), fa::kCacheThreads, 0, stream>>>(p);
   return launch_status();
 }
 

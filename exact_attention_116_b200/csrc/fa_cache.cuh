@@ -20,8 +20,7 @@
 //
 // Both kernels move each byte once, in 16-byte pieces, and are bound by HBM, or by the launch and
 // the chain offsets -> length -> page -> row when there are few rows. One warp takes kCacheWarpElems
-// values of one token for K and for V: the token's place is found once per warp, while the loads
-// of the new rows (which do not wait for it) are in flight.
+// values of one token, of K or of V; the loads of new rows do not wait for the token's place.
 #pragma once
 
 #include "sm100_ptx.cuh"
@@ -29,7 +28,7 @@
 namespace fa {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheWarpElems = 1024;  // of one token's H * d values, K and V each, per warp
+constexpr int kCacheWarpElems = 1024;  // of one token's H * d values, per warp
 constexpr int kScaleMin = 17;          // scale byte of 2^-110
 constexpr int kScaleTop = 247;         // 2^120, the largest a finite row gets
 constexpr int kScaleNan = 255;
@@ -86,67 +85,63 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
 }
 
-// One warp: kCacheWarpElems values of one token. kF8 picks E4M3 pages, D the lanes per row.
+// One warp: kCacheWarpElems values of one token, of K (blockIdx.y = 0) or V. kF8 picks E4M3 pages, D
+// the lanes per row.
 template <int D, bool kF8>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_write_kernel(const CacheParams p) {
   constexpr int kIters = kCacheWarpElems / 256;  // 32 lanes of 8 values
   constexpr int kLanes = D / 8;                  // lanes of one row
   const Abort none{nullptr};
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0 && blockIdx.y == 0)
     report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, threadIdx.x, kCacheThreads);
   const long long unit = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
-  const int lane = lane_id();
+  const int lane = lane_id(), kv = blockIdx.y;
   const int token = (int)(unit / p.parts), part = (int)(unit - (long long)token * p.parts);
   if (token >= p.total) return;
   const int width = p.H * D, first = part * kCacheWarpElems + lane * 8;
-  uint4 x[2][kIters];
+  const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(kv ? p.rows[1] : p.rows[0]) + (long long)token * p.row_stride;
+  void* cache = kv ? p.cache[1] : p.cache[0];
+  uint8_t* scale = kv ? p.scale[1] : p.scale[0];
+  uint4 x[kIters];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int at = first + i * 256;
-      x[kv][i] = make_uint4(0u, 0u, 0u, 0u);
-      if (at < width)
-        x[kv][i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.rows[kv]) +
-                                                        (long long)token * p.row_stride + at));
-    }
+  for (int i = 0; i < kIters; ++i) {
+    const int at = first + i * 256;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (at < width) x[i] = __ldcs(reinterpret_cast<const uint4*>(rows + at));
+  }
   int page = 0, row = 0;
   if (cache_place(p, token, page, row) <= 0) return;
   const long long base = ((long long)page * p.page_size + row) * width;
   const long long size = (long long)p.num_pages * p.page_size * width;
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
+  for (int i = 0; i < kIters; ++i) {
+    const int at = first + i * 256;
+    if constexpr (!kF8) {
+      if (at < width && dbg_range(none, base + at, 8, size))
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + base + at) = x[i];
+    } else {
+      uint32_t most = __vmaxu2(max_abs_bf16x2(x[i].x, x[i].y), max_abs_bf16x2(x[i].z, x[i].w));
 #pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int at = first + i * 256;
-      if constexpr (!kF8) {
-        if (at < width && dbg_range(none, base + at, 8, size))
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.cache[kv]) + base + at) = x[kv][i];
-      } else {
-        uint32_t most = max_abs_bf16x2(x[kv][i].x, x[kv][i].y);
-        most = __vmaxu2(most, max_abs_bf16x2(x[kv][i].z, x[kv][i].w));
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, off));
-        const int s = e4m3_scale_byte(max(most & 0xffffu, most >> 16));
-        // 2^-e = 2^(127 - s): its float exponent field is 254 - s; s = 255 makes every code NaN
-        const float inv = s == kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float((254 - s) << 23);
-        const uint32_t w[4] = {x[kv][i].x, x[kv][i].y, x[kv][i].z, x[kv][i].w};
-        uint2 codes;
-        codes.x = pack_e4m3x4(bf16lo_to_f32(w[0]) * inv, bf16hi_to_f32(w[0]) * inv, bf16lo_to_f32(w[1]) * inv,
-                              bf16hi_to_f32(w[1]) * inv);
-        codes.y = pack_e4m3x4(bf16lo_to_f32(w[2]) * inv, bf16hi_to_f32(w[2]) * inv, bf16lo_to_f32(w[3]) * inv,
-                              bf16hi_to_f32(w[3]) * inv);
-        if (s == kScaleTop) {  // 256 (0x78) becomes 240 (0x77)
-          codes.x = (codes.x & 0x80808080u) | __vminu4(codes.x & 0x7f7f7f7fu, 0x77777777u);
-          codes.y = (codes.y & 0x80808080u) | __vminu4(codes.y & 0x7f7f7f7fu, 0x77777777u);
-        }
-        if (at < width && dbg_range(none, base + at, 8, size)) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.cache[kv]) + base + at) = codes;
-          if ((lane & (kLanes - 1)) == 0)
-            p.scale[kv][((long long)page * p.H + at / D) * p.page_size + row] = (uint8_t)s;
-        }
+      for (int off = kLanes / 2; off > 0; off >>= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, off));
+      const int s = e4m3_scale_byte(max(most & 0xffffu, most >> 16));
+      // 2^-e = 2^(127 - s): its float exponent field is 254 - s; s = 255 makes every code NaN
+      const float inv = s == kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float((254 - s) << 23);
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint2 codes;
+      codes.x = pack_e4m3x4(bf16lo_to_f32(w[0]) * inv, bf16hi_to_f32(w[0]) * inv, bf16lo_to_f32(w[1]) * inv,
+                            bf16hi_to_f32(w[1]) * inv);
+      codes.y = pack_e4m3x4(bf16lo_to_f32(w[2]) * inv, bf16hi_to_f32(w[2]) * inv, bf16lo_to_f32(w[3]) * inv,
+                            bf16hi_to_f32(w[3]) * inv);
+      if (s == kScaleTop) {  // 256 (0x78) becomes 240 (0x77)
+        codes.x = (codes.x & 0x80808080u) | __vminu4(codes.x & 0x7f7f7f7fu, 0x77777777u);
+        codes.y = (codes.y & 0x80808080u) | __vminu4(codes.y & 0x7f7f7f7fu, 0x77777777u);
+      }
+      if (at < width && dbg_range(none, base + at, 8, size)) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + base + at) = codes;
+        if ((lane & (kLanes - 1)) == 0) scale[((long long)page * p.H + at / D) * p.page_size + row] = (uint8_t)s;
       }
     }
+  }
 }
 
 // Two E4M3 codes (16 bits) -> two floats, exactly.
@@ -165,10 +160,10 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const Cach
   constexpr int kVec = kF8 ? 16 : 8;                     // values of a 16-byte piece of a page
   constexpr int kIters = kCacheWarpElems / (32 * kVec);
   const Abort none{nullptr};
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0 && blockIdx.y == 0)
     report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, threadIdx.x, kCacheThreads);
   const long long unit = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
-  const int lane = lane_id();
+  const int lane = lane_id(), kv = blockIdx.y;
   const int token = (int)(unit / p.parts), part = (int)(unit - (long long)token * p.parts);
   if (token >= p.total) return;
   int page = 0, row = 0;
@@ -177,46 +172,42 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const Cach
   const int width = p.H * D, first = part * kCacheWarpElems + lane * kVec;
   const long long base = ((long long)page * p.page_size + row) * width;
   const long long size = (long long)p.num_pages * p.page_size * width;
-  uint4 x[2][kIters];
-  int s[2][kIters];
+  const char* cache = static_cast<const char*>(kv ? p.cache[1] : p.cache[0]);
+  const uint8_t* scale = kv ? p.scale[1] : p.scale[0];
+  __nv_bfloat16* rows = static_cast<__nv_bfloat16*>(kv ? p.rows[1] : p.rows[0]) + (long long)token * p.row_stride;
+  uint4 x[kIters];
+  int s[kIters];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int at = first + i * 32 * kVec;
-      x[kv][i] = make_uint4(0u, 0u, 0u, 0u);
-      s[kv][i] = kScaleMin;
-      if (placed && at < width && dbg_range(none, base + at, kVec, size)) {
-        const char* c = static_cast<const char*>(p.cache[kv]);
-        x[kv][i] = *reinterpret_cast<const uint4*>(c + (base + at) * (kF8 ? 1 : 2));
-        if (kF8) s[kv][i] = p.scale[kv][((long long)page * p.H + at / D) * p.page_size + row];
-      }
+  for (int i = 0; i < kIters; ++i) {
+    const int at = first + i * 32 * kVec;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    s[i] = kScaleMin;
+    if (placed && at < width && dbg_range(none, base + at, kVec, size)) {
+      x[i] = __ldcs(reinterpret_cast<const uint4*>(cache + (base + at) * (kF8 ? 1 : 2)));
+      if (kF8) s[i] = scale[((long long)page * p.H + at / D) * p.page_size + row];
     }
+  }
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
+  for (int i = 0; i < kIters; ++i) {
+    const int at = first + i * 32 * kVec;
+    if (at >= width) continue;
+    if constexpr (!kF8) {
+      __stcs(reinterpret_cast<uint4*>(rows + at), x[i]);
+    } else {
+      // 2^(s - 127); a scale byte below 1 would need a subnormal float: no row is written with one
+      const float unit_f = s[i] == kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float(max(s[i], 1) << 23);
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t r[8];
 #pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int at = first + i * 32 * kVec;
-      if (at >= width) continue;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.rows[kv]) + (long long)token * p.row_stride + at;
-      if constexpr (!kF8) {
-        *reinterpret_cast<uint4*>(out) = x[kv][i];
-      } else {
-        // 2^(s - 127); a scale byte below 1 would need a subnormal float: no row is written with one
-        const float unit_f =
-            s[kv][i] == kScaleNan ? __int_as_float(0x7fc00000) : __int_as_float(max(s[kv][i], 1) << 23);
-        const uint32_t w[4] = {x[kv][i].x, x[kv][i].y, x[kv][i].z, x[kv][i].w};
-        uint32_t r[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 a = e4m3x2_to_f32(w[e] & 0xffffu), c = e4m3x2_to_f32(w[e] >> 16);
-          r[2 * e] = pack_bf16x2(a.x * unit_f, a.y * unit_f);
-          r[2 * e + 1] = pack_bf16x2(c.x * unit_f, c.y * unit_f);
-        }
-        *reinterpret_cast<uint4*>(out) = make_uint4(r[0], r[1], r[2], r[3]);
-        *reinterpret_cast<uint4*>(out + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = e4m3x2_to_f32(w[e] & 0xffffu), c = e4m3x2_to_f32(w[e] >> 16);
+        r[2 * e] = pack_bf16x2(a.x * unit_f, a.y * unit_f);
+        r[2 * e + 1] = pack_bf16x2(c.x * unit_f, c.y * unit_f);
       }
+      __stcs(reinterpret_cast<uint4*>(rows + at), make_uint4(r[0], r[1], r[2], r[3]));
+      __stcs(reinterpret_cast<uint4*>(rows + at + 8), make_uint4(r[4], r[5], r[6], r[7]));
     }
+  }
 }
 
 }  // namespace fa

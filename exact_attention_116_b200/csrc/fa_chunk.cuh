@@ -934,13 +934,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       constexpr int kRowStep = Cfg::kConvThreads / kPerRow;
       const int ct = tid - 128 - Cfg::kSoftThreads;
       const int c = ct % kPerRow;      // this thread's piece, in rows ct / kPerRow + k * kRowStep
-      const int box_shift = 31 - __clz(p.box_rows);
+      const int box_shift = 31 - __clz(p.box_rows), odd = c >> 2;
       uint32_t n = 0;
       const ChunkBlock* block;
       for (uint32_t i = 0; (block = chunk_take(bars, i, ab)); ++i) {
         const ChunkBlock& w = *block;
         for (int v = w.v0; v < w.v1; ++v) {
           const int key0 = w.keys.tile(v) * 128;
+          const int hi = w.keys.vis_hi - key0, lo = w.keys.vis_lo - key0, sinks = p.sinks - key0;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const uint32_t rs = n % Cfg::kRawSlots, ks = n % Cfg::kSlots;
@@ -949,13 +950,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
             const uint8_t* raw = smem_gen + Cfg::kOffRaw + rs * Cfg::kRawSlotBytes;
             const uint8_t* scale = raw + Cfg::kRawBytes;
             const uint32_t dst = sKV + ks * Cfg::kTileBytes;
+            // (all loads ahead of the stores, which the compiler would keep them behind)
+            uint4 xs[128 / kRowStep];
+            uint32_t ss[128 / kRowStep];
 #pragma unroll
             for (int k = 0; k < 128 / kRowStep; ++k) {
-              const int row = ct / kPerRow + k * kRowStep, key = key0 + row;
-              uint4 x = reinterpret_cast<const uint4*>(raw)[row * kPerRow + c];
-              uint32_t s = scale[((row >> box_shift) << 7) + (row & (p.box_rows - 1))];
+              const int row = ct / kPerRow + k * kRowStep;
+              xs[k] = reinterpret_cast<const uint4*>(raw)[row * kPerRow + c];
+              ss[k] = scale[((row >> box_shift) << 7) + (row & (p.box_rows - 1))];
+            }
+#pragma unroll
+            for (int k = 0; k < 128 / kRowStep; ++k) {
+              const int row = ct / kPerRow + k * kRowStep;
+              uint4 x = xs[k];
+              uint32_t s = ss[k];
               // V rows that no row of the block sees may hold anything: 0 (their weights are 0)
-              if (kv && (key > w.keys.vis_hi || (key < w.keys.vis_lo && key >= p.sinks))) {
+              if (kv && (row > hi || (row < lo && row >= sinks))) {
                 x = make_uint4(0u, 0u, 0u, 0u);
                 s = 127u;
               }
@@ -972,17 +982,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) r[e] = mul_bf16x2(r[e], g | (g << 16));
               }
-              // two 16-byte chunks; the upper half of a row's threads stores its odd chunk first,
-              // so that the eight threads of a row (d = 128) touch all banks in each store
-              const uint32_t b0 = dst + (uint32_t)(c >> 2) * 16384u;
-              const uint32_t a0 = b0 + sw128_offset(row, 2 * (c & 3)), a1 = b0 + sw128_offset(row, 2 * (c & 3) + 1);
-              if (c & 4) {
-                st_shared_v4(a1, r[4], r[5], r[6], r[7]);
-                st_shared_v4(a0, r[0], r[1], r[2], r[3]);
-              } else {
-                st_shared_v4(a0, r[0], r[1], r[2], r[3]);
-                st_shared_v4(a1, r[4], r[5], r[6], r[7]);
-              }
+              // two 16-byte chunks; the upper half of a row's threads stores its odd chunk first, so
+              // that the eight threads of a row (d = 128) touch all banks in each store
+              const uint32_t to = dst + (uint32_t)(c >> 2) * 16384u + row * 128;
+              const uint32_t a0 = to + (((2 * (c & 3) + odd) ^ (row & 7)) << 4), a1 = to + (((2 * (c & 3) + 1 - odd) ^ (row & 7)) << 4);
+              st_shared_v4(a0, odd ? r[4] : r[0], odd ? r[5] : r[1], odd ? r[6] : r[2], odd ? r[7] : r[3]);
+              st_shared_v4(a1, odd ? r[0] : r[4], odd ? r[1] : r[5], odd ? r[2] : r[6], odd ? r[3] : r[7]);
             }
             fence_proxy_async_smem();
             __syncwarp();

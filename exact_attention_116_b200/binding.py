@@ -580,10 +580,12 @@ def cache_read_paged(k_cache, v_cache, block_table, seqlens, cu_seqlens, total, 
     if k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be (num_pages, page_size, heads, head_dim), of equal shape")
     H, d = k_cache.shape[2:]
-    k = torch.empty_strided((total, H, d), (max(H * d, 1), max(d, 1), 1), dtype=torch.bfloat16, device=k_cache.device)
-    v = torch.empty_like(k)
-    if stream is not None:
-        _used_on(stream, k, v)
+
+    def make():
+        k = torch.empty_strided((total, H, d), (max(H * d, 1), max(d, 1), 1), dtype=torch.bfloat16, device=k_cache.device)
+        return k, torch.empty_like(k)
+
+    k, v = _outputs_on(stream, k_cache.device, make)
     cache_read_paged_into(k_cache, v_cache, block_table, seqlens, cu_seqlens, k, v, k_scale, v_scale, stream)
     return k, v
 
@@ -595,11 +597,18 @@ def _int32(x, name: str) -> int:
     return x
 
 
-def _used_on(stream, *new: torch.Tensor) -> None:
-    """Tensors made here are not handed out again before work on `stream` is done."""
+def _outputs_on(stream, device, make):
+    """make()'s tensors for a call on `stream` (None: the current one). They are `stream`'s own, so that no
+    memory which the current stream still uses is among them, and are kept until the current stream, where the
+    caller goes on with them, has done what it had been given when they are freed."""
+    if stream is None or device.type != "cuda":
+        return make()
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        new = make()
     for t in new:
-        if t.is_cuda:
-            t.record_stream(stream)
+        t.record_stream(current)
+    return new
 
 
 def chunk_workspace_bytes(B: int, total: int, Hq: int, Hkv: int, d: int) -> int:
@@ -634,9 +643,11 @@ def chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, l
         raise ValueError(f"the {Hq} query heads must be a multiple of the cache's {Hkv}")
     if workspace is None:
         wb = _chunk_workspace(index, B, total, Hq, Hkv, d)
-        workspace = torch.empty_strided((wb,), (1,), dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            _used_on(stream, workspace)
+        if stream is None:
+            workspace = torch.empty_strided((wb,), (1,), dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):  # its own memory: free for the stream's next call when this one is done
+                workspace = torch.empty_strided((wb,), (1,), dtype=torch.uint8, device=q.device)
         ws = workspace.data_ptr()
     else:
         if workspace.get_device() != index:
@@ -660,11 +671,13 @@ def attention_chunk_paged(q, k_cache, v_cache, block_table, seqlens, cu_seqlens,
     window. Rows from cu_seqlens[B] on are not initialised (chunk_paged_into leaves them as they were)."""
     if q.dim() != 3:
         raise ValueError("q must be a (total, heads, head_dim) bfloat16 CUDA tensor")
-    o = torch.empty_like(q, memory_format=torch.contiguous_format)
     total, Hq, _ = q.shape
-    lse = torch.empty_strided((Hq, total), (max(total, 1), 1), dtype=torch.float32, device=q.device)
-    if stream is not None:
-        _used_on(stream, o, lse)
+
+    def make():
+        return (torch.empty_like(q, memory_format=torch.contiguous_format),
+                torch.empty_strided((Hq, total), (max(total, 1), 1), dtype=torch.float32, device=q.device))
+
+    o, lse = _outputs_on(stream, q.device, make)
     chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, lse, scale, causal, window, sinks,
                      k_scale, v_scale, None, stream)
     return o, lse

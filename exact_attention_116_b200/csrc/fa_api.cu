@@ -599,8 +599,9 @@ int cache_rows(void* k_rows, void* v_rows, long long row_stride, void* k_cache, 
   const Span rows[2] = {{k_rows, rb}, {v_rows, rb}};
   const Span plan[3] = {{block_table, (size_t)B * max_pages * 4}, {seqlens, (size_t)B * 4}, {cu, (size_t)(B + 1) * 4}};
   for (int i = 0; i < 4; ++i) {
-    if (any_overlap(caches[i], rows, 2) || any_overlap(caches[i], caches + i + 1, 3 - i)) return FA_ERR_INVALID_ARG;
-    if (kWrite && any_overlap(caches[i], plan, 3)) return FA_ERR_INVALID_ARG;
+    if (any_overlap(caches[i], rows, 2)) return FA_ERR_INVALID_ARG;
+    if (kWrite && (any_overlap(caches[i], caches + i + 1, 3 - i) || any_overlap(caches[i], plan, 3)))
+      return FA_ERR_INVALID_ARG;
   }
   if (!kWrite && (any_overlap(rows[0], plan, 3) || any_overlap(rows[1], plan, 3))) return FA_ERR_INVALID_ARG;
   // (K and V rows may be slices of one tensor: their spans interleave. Read back, they must not.)

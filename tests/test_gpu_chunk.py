@@ -386,3 +386,78 @@ def test_no_rows():
     fa.chunk_paged_into(t["q"], t["k"], t["v"], t["table"], t["lens"], t["cu"], o, lse)
     fa.check()
     assert (o == 1).all() and (lse == 1).all()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_the_log_sum_exp_is_an_fp32_output(f8):
+    """Relative to its own size, over rows of a few keys and of many. A score is a sum of d exact products, each
+    of the at most d additions off by 2^-24 of the partial sum (|partial sums| <= sum |q k| scale, here at most
+    128 * 12 / 11 = 140 and 20 times a score's size at most), and is scaled and rounded twice more; the
+    exponentials are off by 2.5e-7, a sum of n of them by (n / 64 + 64) 2^-24 (64 added in order, then tiles),
+    the logarithm by 2^-22: 2e-5 in all for an LSE of order 1 and more."""
+    for new, keys, Hq, Hkv in (([7], [7], 4, 4), ([1, 2, 3], [1, 5, 40], 8, 2), ([1, 1], [3000, 90], 4, 1),
+                               ([150, 1], [700, 300], 4, 2)):
+        b = Batch(new, keys, Hq, Hkv, 128, 16, f8, seed=len(new))
+        o, lse = call(b.gpu())
+        fa.check()
+        ref = b.reference(128 ** -0.5, True, (-1, -1), 0)[1]
+        err = np.linalg.norm(np64(lse) - ref) / np.linalg.norm(ref)
+        assert err <= 2e-5, err
+        assert np.abs(np64(lse) - ref).max() <= 2e-5 * max(1.0, np.abs(ref).max())
+
+
+def test_results_on_a_side_stream_need_no_more_than_its_events():
+    """Calls that allocate their results and workspace for another stream, while the current one frees and
+    reuses memory of the same sizes."""
+    b = Batch([200, 1], [900, 3000], 8, 2, 128, 32, False, seed=77)
+    t = b.gpu()
+    alone = call(t)
+    rk, rv = fa.cache_read_paged(t["k"], t["v"], t["table"], t["lens"], t["cu"], b.total)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        junk = [torch.full_like(t["q"], 5.0) for _ in range(3)] + [torch.full((8, b.total), 9.0, device="cuda")]
+        del junk
+        o, lse = call(t, stream=side)
+        k, v = fa.cache_read_paged(t["k"], t["v"], t["table"], t["lens"], t["cu"], b.total, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        same = torch.equal(o, alone[0]) and torch.equal(lse, alone[1]) and torch.equal(k, rk) and torch.equal(v, rv)
+        assert same
+        del o, lse, k, v
+    fa.check()
+
+
+def test_refusals_of_the_binding():
+    b = Batch([4, 1], [40, 20], 4, 2, 64, 16, False, seed=5)
+    f = Batch([4, 1], [40, 20], 4, 2, 64, 16, True, seed=5)
+    t, u = b.gpu(), f.gpu()
+    bad = [dict(q=t["q"].float()), dict(q=t["q"][:, :3]), dict(q=t["q"][..., ::2]), dict(k=t["k"].transpose(1, 2)),
+           dict(k=t["k"][:, :8]), dict(v=t["v"].float()), dict(table=t["table"].long()), dict(lens=t["lens"][:1]),
+           dict(cu=t["cu"][:2]), dict(table=t["table"][0]), dict(lens=t["lens"].cpu()), dict(ks=u["ks"], vs=None),
+           dict(ks=u["ks"], vs=u["vs"]), dict(cu=t["cu"].repeat(2)[::2])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            call(dict(t, **kw))
+    for kw in (dict(ks=None, vs=None), dict(ks=u["ks"].transpose(1, 2)), dict(vs=u["vs"][:1]), dict(ks=u["ks"].int())):
+        with pytest.raises(ValueError):
+            call(dict(u, **kw))
+    o, lse = torch.empty_like(t["q"]), torch.empty(4, 5, device="cuda")
+    for oo, ll in ((o.float(), lse), (o[:4], lse), (o, lse.t().contiguous()), (o, lse.double()), (o, lse[:, ::2])):
+        with pytest.raises(ValueError):
+            fa.chunk_paged_into(t["q"], t["k"], t["v"], t["table"], t["lens"], t["cu"], oo, ll)
+    with pytest.raises(fa.FaError):  # the output over the queries
+        fa.chunk_paged_into(t["q"], t["k"], t["v"], t["table"], t["lens"], t["cu"], t["q"], lse)
+    with pytest.raises(fa.FaError):  # a workspace that is too small
+        fa.chunk_paged_into(t["q"], t["k"], t["v"], t["table"], t["lens"], t["cu"], o, lse,
+                            workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises((ValueError, fa.FaError)):
+        call(t, window=(2 ** 40, -1))
+    with pytest.raises(fa.FaError):
+        call(t, sinks=-1)
+    rows = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for kn, vn in ((rows, rows[:4]), (rows.half(), rows.half()), (rows[:, :1], rows[:, :1])):
+        with pytest.raises(ValueError):
+            fa.cache_write_paged(kn, vn, t["k"], t["v"], t["table"], t["lens"], t["cu"])
+    with pytest.raises(fa.FaError):  # K and V written to the same pages
+        fa.cache_write_paged(rows, rows.clone(), t["k"], t["k"], t["table"], t["lens"], t["cu"])
+    fa.check()

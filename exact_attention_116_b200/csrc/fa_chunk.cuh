@@ -82,8 +82,9 @@ struct ChunkCfg {
   static constexpr int kThreads = 128 + kSoftThreads + kConvThreads;
   static constexpr int kBlockReaders = 2 + kSoftWarps + kConvThreads / 32;  // the loads', the MMAs', ...
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;  // a thread's at launch
-  static constexpr int kLoadRegs = 56, kConvRegs = kTiles == 2 ? 48 : 64;
-  static constexpr int kSoftRegs = kTiles == 2 ? (kF8 ? 88 : 104) : kF8 ? 128 : 0;  // 0: as launched
+  // (the load and MMA roles spill below 80: 56 cost more there than 104 gained the softmax)
+  static constexpr int kLoadRegs = kF8 && kTiles == 2 ? 56 : 80, kConvRegs = kTiles == 2 ? 48 : 64;
+  static constexpr int kSoftRegs = kTiles == 2 ? (kF8 ? 88 : 96) : kF8 ? 128 : 0;  // 0: as launched
   static_assert(kSoftRegs * kSoftThreads + kLoadRegs * 128 + kConvRegs * kConvThreads <= kRegs * kThreads, "registers");
   static constexpr int kBoxes = D / 64;               // 128-byte boxes per bf16 row
   static constexpr int kTileBytes = 128 * D * 2;      // a bf16 tile of Q, K or V
@@ -440,28 +441,10 @@ __device__ __forceinline__ void chunk_visible(int kbase, int kmin, int kmax, int
     m[w] = (bits_below(end - 32 * w) & ~bits_below(from - 32 * w)) | bits_below(first - 32 * w);
 }
 
-// 2^x of a pair on the FMA pipe, as exp2_poly2 with a degree-5 polynomial (relative error 6e-8 of
-// the fit, 2e-7 with its float32 steps: that of ex2.approx): the log-sum-exp, an fp32 output, would
-// show the degree-3 polynomial's 7.5e-5 in rows of a few keys.
-constexpr float kExp2D0 = 1.000000051e+00f, kExp2D1 = 6.931467120e-01f, kExp2D2 = 2.402214209e-01f,
-                kExp2D3 = 5.551047092e-02f, kExp2D4 = 9.675267120e-03f, kExp2D5 = 1.318565354e-03f;
-__device__ __forceinline__ float2 exp2_poly5x2(float2 x_in) {
-  const float2 x = make_float2(fmaxf(x_in.x, -125.0f), fmaxf(x_in.y, -125.0f));
-  const float2 t = add2(x, make_float2(12582912.0f, 12582912.0f));
-  const float2 jf = add2(t, make_float2(-12582912.0f, -12582912.0f));
-  const float2 f = fma2(jf, make_float2(-1.0f, -1.0f), x);
-  float2 p = fma2(make_float2(kExp2D5, kExp2D5), f, make_float2(kExp2D4, kExp2D4));
-  p = fma2(p, f, make_float2(kExp2D3, kExp2D3));
-  p = fma2(p, f, make_float2(kExp2D2, kExp2D2));
-  p = fma2(p, f, make_float2(kExp2D1, kExp2D1));
-  p = fma2(p, f, make_float2(kExp2D0, kExp2D0));
-  const float rx = __int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23));
-  const float ry = __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23));
-  return make_float2(x_in.x >= -125.0f ? rx : 0.0f, x_in.y >= -125.0f ? ry : 0.0f);
-}
-
 // Exponentials of 32 scores (16 pairs from pair k0 on) against the reference maximum, packed to bf16
-// pairs and summed twice, as fwd_exp_chunk; one pair in eight takes the polynomial.
+// pairs and summed twice, as fwd_exp_chunk, but all on MUFU: the forward's degree-3 polynomial (off by
+// 7.5e-5) would show in the log-sum-exp of rows of a few keys, and a degree-5 one for one pair in four,
+// eight or sixteen was not faster here (111 to 117 us against 111, mixed chunks over E4M3 pages).
 template <bool kPosScale, int kC>
 __device__ __forceinline__ void chunk_exp(const float (&x)[kC], int k0, float c, float m_use, uint32_t (&pk)[16],
                                           float2& sum, float2& rsum) {
@@ -470,7 +453,7 @@ __device__ __forceinline__ void chunk_exp(const float (&x)[kC], int k0, float c,
   for (int k = 0; k < 16; ++k) {
     const float2 xv = make_float2(x[2 * (k0 + k)], x[2 * (k0 + k) + 1]);
     const float2 a = kPosScale ? fma2(xv, c2, neg_m) : add2(xv, neg_m);
-    const float2 pv = k % 8 == 0 ? exp2_poly5x2(a) : make_float2(ex2_approx(a.x), ex2_approx(a.y));
+    const float2 pv = make_float2(ex2_approx(a.x), ex2_approx(a.y));
     sum = add2(sum, pv);
     pk[k] = pack_bf16x2(pv.x, pv.y);
     rsum = add_bf16x2_f32x2(pk[k], rsum);

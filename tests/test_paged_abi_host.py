@@ -163,28 +163,6 @@ def test_fast_division():
         assert np.array_equal(got, n // np.uint64(d)) and int((n + (n * np.uint64(m) >> np.uint64(32))).max()) < 1 << 32
 
 
-def test_degree_5_exp2():
-    """The polynomial of the chunk kernel: the fitted coefficients, and its float32 steps within 2.5e-7."""
-    import importlib.util
-    csrc = os.path.join(ROOT, "exact_attention_116_b200", "csrc")
-    spec = importlib.util.spec_from_file_location("fit_exp2_poly", os.path.join(csrc, "fit_exp2_poly.py"))
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    with open(os.path.join(csrc, "fa_chunk.cuh")) as f:
-        text = f.read()
-    c = [np.float32(re.search(rf"kExp2D{k} = ([0-9.e+-]+)f", text).group(1)) for k in range(6)]
-    fitted = mod.f32_coeffs(5)
-    assert all(abs(float(a) - float(b)) <= 3e-7 * abs(float(a)) for a, b in zip(fitted, c))
-    x = np.concatenate([np.linspace(-125, 8, 1_000_001), [-0.5, 0.5, 1.5, 0.0]]).astype(np.float32)
-    t = (x + np.float32(12582912.0)).astype(np.float32)
-    f = (x - (t - np.float32(12582912.0))).astype(np.float64)
-    p = np.float32(c[5])
-    for k in (4, 3, 2, 1, 0):  # fused multiply-adds: one rounding each
-        p = (np.float64(p) * f + np.float64(c[k])).astype(np.float32)
-    r = (p.view(np.int32) + (t.view(np.int32) << 23)).view(np.float32)
-    assert np.abs(r.astype(np.float64) / np.exp2(x.astype(np.float64)) - 1).max() <= 2.5e-7
-
-
 @pytest.mark.parametrize("seed", range(6))
 def test_pieces_cover_every_tile_once(seed):
     """A model of the work split: pieces of a list of T tiles, the blocks they cut, and their partials' slots."""

@@ -670,29 +670,26 @@ int make_map_scales(CUtensorMap* m, const void* base, int num_pages, int page_si
   return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// One or two 128-row tiles per block of the chunk kernel: two share every K/V load, which long
-// chunks need; with at most one tile of rows per sequence on average the second would stand idle.
-int chunk_tiles(int B, int total, int G) { return (double)total * G <= 128.0 * B ? 1 : 2; }
+// One or two 128-row tiles per block of the chunk kernel: two share every K/V load, which long chunks
+// need; with few rows to a sequence the second would stand idle. Measured with one / two (us, bf16
+// pages, 8 sequences): 1 row over 6000 keys 74.6 / 78.8; over 4000 keys 64 rows 41.6 / 41.5, 128 rows
+// 47.0 / 43.8, 256 rows 70.5 / 55.6; two chunks of 1024 tokens x 4 heads 170 / 130.
+int chunk_tiles(int B, int total, int G) { return (double)total * G <= 64.0 * B ? 1 : 2; }
 
-fa::FastDiv fast_div(unsigned d) {
-  unsigned s = 0;
-  while ((1ull << s) < d) ++s;
-  return {(unsigned)((((1ull << 32) << s) + d - 1) / d - (1ull << 32)), s};
-}
-
-// Rows of a few tokens over E4M3 pages take the transposed kernel: when a sequence's rows fit its
-// 16-row blocks on average (a longer chunk in such a batch is cut into several, which read its keys
-// again).
 // Heads whose CTAs run next to each other: the most of 4, 2 and 1 that divides the heads and the SMs.
-#ifndef FA_HG
-#define FA_HG 4
-#endif
+// Measured with 1 / 2 / 4 heads (us): a step of 8 sequences of 4096 to 8192 keys, 16 heads, bf16 pages
+// 76.9 / 77.0 / 75.3; 16 rows over 131072 keys, 8 heads 100 / 98.4 / 97.0; a step of 48 sequences, 8
+// heads, E4M3 pages (128-byte rows) 223 / 207 / 207.
 int chunk_head_group(int Hkv, int sms) {
-  for (int hg = FA_HG; hg > 1; hg /= 2)
+  for (int hg = 4; hg > 1; hg /= 2)
     if (Hkv % hg == 0 && sms % hg == 0) return hg;
   return 1;
 }
 
+// Rows of a few tokens over E4M3 pages take the transposed kernel: when a sequence's rows fit its
+// 16-row blocks on average (a longer chunk in such a batch is cut into several, which read its keys
+// again). A step of 48 sequences of 2000 to 15630 keys, 4 query heads to each of 8: 153 us, 450 with
+// fa_chunk_kernel.
 bool chunk_few(bool f8, int d, int B, int total, int G) {
   return f8 && d == fa::kFewD && G <= fa::kFewRows && (double)total <= (double)B * (fa::kFewRows / G);
 }

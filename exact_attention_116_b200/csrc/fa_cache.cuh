@@ -21,6 +21,10 @@
 // Both kernels move each byte once, in 16-byte pieces, and are bound by HBM, or by the launch and
 // the chain offsets -> length -> page -> row when there are few rows. One warp takes kCacheWarpElems
 // values of one token, of K or of V; the loads of new rows do not wait for the token's place.
+// Measured: reading 49573 tokens of 16 heads x 128 back 97 to 103 us (609 MB, 95 at the copy rate; K and
+// V by one warp 112, 512 values a warp 118, no streaming hints 101); writing 16625 tokens of 8 heads
+// 22.6 us (102 MB, 15.8 at the copy rate, and a launch; finding the places and the scattered scale
+// bytes cost 2 us each); a step's 64 tokens 4.2 us, a launch and its chain.
 #pragma once
 
 #include "sm100_ptx.cuh"

@@ -18,8 +18,8 @@
 // hg CTAs, one for each head of the group, next to each other; in all one CTA per SM. So every CTA
 // visits the same number of key tiles (within one), for decoding steps, long prompts and mixtures
 // alike, and the heads' rows of a token, which lie side by side in a page, are read at about the
-// same time: DRAM and L2 serve 512 bytes and more at a stretch, not 128 or 256 (measured at
-// fa_chunk_few_kernel). A block that lies in one piece is finished by its CTA;
+// same time: DRAM serves 512 bytes and more at a stretch, not 128 or 256. A block that lies in one
+// piece is finished by its CTA;
 // otherwise each of its pieces writes a partial (O / l, log2 l + m) and fa_chunk_merge_kernel joins
 // them by their log-sum-exp. (The CTA that finished a block last used to join it: one CTA reading
 // all partials of 64 rows took 60 us of a 178 us call, 32 query heads over 131072 keys.)
@@ -30,9 +30,21 @@
 // the rounded weights.
 //
 // E4M3 pages (kF8): the codes of a K or V tile and their power-of-two scales are loaded as they
-// are, and four warps write the tile's values, code * 2^e, as bf16 into the operand buffers: exact,
+// are, and eight warps write the tile's values, code * 2^e, as bf16 into the operand buffers: exact,
 // since a code has 4 significant bits. The products then are those of bf16 pages holding these
-// values; 8-bit products would have to round Q and P to 4 bits.
+// values, bit for bit; 8-bit products would have to split Q and P into three terms each, which pays
+// for few rows (fa_chunk_few.cuh) and not where the tensor core and the softmax set the pace.
+//
+// What bounds it: over bf16 pages few rows read the cache at 1.40 us a tile of 128 keys (64 KB a
+// CTA, 6.9 TB/s in all); two tiles of rows take 2.2 us a key tile at d = 128 (1130 TFLOP/s, the
+// forward's rate: the softmax's instruction stream, tensor pipe 58%) and 2.1 at d = 64; over E4M3
+// pages 2.9, of which the conversion's arithmetic is 0.5 (without it 2.3). A call adds 12 to 25 us:
+// launch 3, set-up until the first scores 6 (cold instructions), first tile 1.5, join 3 to 8.
+// Measured steps: one thread that walks over the blocks for all roles in place of every role (63 ->
+// 46 us, window with sinks, with the masks as bits); the page entry of the next tile read one tile
+// ahead (144 -> 120 us, mixed chunks over E4M3 pages); set-up by four warps and not all (5 us).
+// Not kept: K and V converted by four warps each (rings of one and two tiles: 3.3 us for 2.4),
+// blocks weighted by their rows in the work split (116 us for 113).
 #pragma once
 
 #include "fa_cache.cuh"
@@ -77,7 +89,7 @@ template <int D, bool kF8, int kTiles>
 struct ChunkCfg {
   static constexpr int kSoftWarps = 8 * kTiles;       // row split: two warps per 32 rows
   static constexpr int kSoftThreads = 32 * kSoftWarps;
-  static constexpr int kConvThreads = kF8 ? 256 : 0;
+  static constexpr int kConvThreads = kF8 ? 256 : 0;  // (with 128: 2.7 us a tile for 2.4)
   static constexpr int kConvWarps = kConvThreads / 32;
   static constexpr int kThreads = 128 + kSoftThreads + kConvThreads;
   static constexpr int kBlockReaders = 2 + kSoftWarps + kConvThreads / 32;  // the loads', the MMAs', ...

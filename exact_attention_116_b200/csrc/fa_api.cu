@@ -694,6 +694,13 @@ bool chunk_few(bool f8, int d, int B, int total, int G) {
   return f8 && d == fa::kFewD && G <= fa::kFewRows && (double)total <= (double)B * (fa::kFewRows / G);
 }
 
+// (fa::FastDiv says what the numbers are)
+fa::FastDiv fast_div(unsigned d) {
+  unsigned s = 0;
+  while ((1ull << s) < d) ++s;
+  return {(unsigned)((((1ull << 32) << s) + d - 1) / d - (1ull << 32)), s};
+}
+
 struct ChunkWorkspace {
   size_t o_bytes, lse_bytes, split_bytes;
   size_t bytes() const { return o_bytes + lse_bytes + split_bytes; }

@@ -542,7 +542,7 @@ def cache_write_paged(k_new, v_new, k_cache, v_cache, block_table, seqlens, cu_s
                       stream=None) -> None:
     """fa_cache_write: write the packed new rows k_new, v_new (total, H, d) bf16 into their pages, in place.
     Sequence b's rows [cu_seqlens[b], cu_seqlens[b + 1]) are the last of its seqlens[b] positions; rows from
-    cu_seqlens[B] on are not read. k_cache, v_cache: (num_pages, page_size, H, d) bf16, or E4M3
+    cu_seqlens[B] on are not written. k_cache, v_cache: (num_pages, page_size, H, d) bf16, or E4M3
     (float8_e4m3fn or uint8) with k_scale, v_scale (num_pages, H, page_size) E8M0 bytes (uint8 or
     float8_e8m0fnu): then each (token, head) row is quantised with its own power-of-two scale."""
     index = _cuda_index(k_new)
@@ -642,7 +642,7 @@ def chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, l
     if Hq == 0 or Hkv == 0 or Hq % Hkv:
         raise ValueError(f"the {Hq} query heads must be a multiple of the cache's {Hkv}")
     if workspace is None:
-        wb = _chunk_workspace(index, B, total, Hq, Hkv, d)
+        wb = _chunk_workspace(index, B, total, Hq, Hkv, d) or chunk_workspace_bytes(B, total, Hq, Hkv, d)
         if stream is None:
             workspace = torch.empty_strided((wb,), (1,), dtype=torch.uint8, device=q.device)
         else:

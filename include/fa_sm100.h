@@ -175,7 +175,7 @@ int fa_decode_paged(const void* q, void* k_cache, void* v_cache, const void* k_n
  *   cu_seqlens   device (B+1) int32: sequence b's new rows are the packed rows
  *                [cu_seqlens[b], cu_seqlens[b+1]); cu_seqlens[0] = 0, non-decreasing,
  *                cu_seqlens[B] <= total. Rows from cu_seqlens[B] on belong to no sequence:
- *                they are not read, and the outputs' are left as they were.
+ *                they may hold anything, and the outputs' are left as they were.
  *   seqlens      device (B) int32: keys of sequence b, its new rows included: row i of its new_b
  *                rows sits at position seqlens[b] - new_b + i (a negative position has no place).
  *   block_table  device (B,max_pages) int32, as fa_decode_paged; entries past a sequence's

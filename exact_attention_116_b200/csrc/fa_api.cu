@@ -563,6 +563,28 @@ size_t rows_bytes(int total, size_t width, long long stride) {
   return total < 1 ? 0 : ((size_t)(total - 1) * (size_t)stride + width) * 2;
 }
 
+// A launch that may begin while the kernel before it on the stream ends (its kernels wait for that one
+// before they touch global memory, in every thread, so that the end of one implies the end of those
+// before it). It saves 2 us a call: a step over bf16 pages 76.9 -> 74.6 us, a read of 609 MB 98.8 -> 96.5.
+template <class... Params, class... Args>
+int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
 template <bool kWrite>
 int launch_cache(const fa::CacheParams& p, int d, cudaStream_t stream) {
   const long long units = (long long)p.total * p.parts, per_block = fa::kCacheThreads / 32;
@@ -576,8 +598,7 @@ int launch_cache(const fa::CacheParams& p, int d, cudaStream_t stream) {
   else
     kernel = d == 64 ? (f8 ? fa::fa_cache_read_kernel<64, true> : fa::fa_cache_read_kernel<64, false>)
                      : (f8 ? fa::fa_cache_read_kernel<128, true> : fa::fa_cache_read_kernel<128, false>);
-  kernel<<<dim3((unsigned)blocks, 2), fa::kCacheThreads, 0, stream>>>(p);
-  return launch_status();
+  return launch_dependent(kernel, dim3((unsigned)blocks, 2), fa::kCacheThreads, 0, stream, p);
 }
 
 // Writing (kWrite) or reading the rows [cu[b], cu[b + 1]) of every sequence.
@@ -713,28 +734,17 @@ ChunkWorkspace chunk_workspace(int pieces, int tiles, int d) {
 template <int D, bool kF8, int kTiles>
 int chunk_launch(int grid, const CUtensorMap* m, const fa::ChunkParams& p, cudaStream_t stream) {
   using Cfg = fa::ChunkCfg<D, kF8, kTiles>;
-  fa::fa_chunk_kernel<D, kF8, kTiles><<<grid, Cfg::kThreads, Cfg::kSmemBytes, stream>>>(m[0], m[1], m[2], m[3], m[4], p);
-  return launch_status();
+  return launch_dependent(fa::fa_chunk_kernel<D, kF8, kTiles>, dim3(grid), Cfg::kThreads, Cfg::kSmemBytes, stream, m[0],
+                          m[1], m[2], m[3], m[4], p);
 }
 
 // The join of blocks that are spread over several pieces, as the main kernel's programmatic dependent.
 template <int D, int kTiles>
 int chunk_merge_launch(int ctas, const fa::ChunkParams& p, cudaStream_t stream) {
   const long long rows = std::min<long long>((long long)p.total * p.G, kTiles * 128);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (unsigned)((rows + fa::kMergeRows - 1) / fa::kMergeRows));
-  cfg.blockDim = dim3(fa::kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fa::fa_chunk_merge_kernel<D, kTiles>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return FA_ERR_CUDA;
-  }
-  return FA_OK;
+  return launch_dependent(fa::fa_chunk_merge_kernel<D, kTiles>,
+                          dim3(ctas, (unsigned)((rows + fa::kMergeRows - 1) / fa::kMergeRows)), fa::kMergeThreads, 0,
+                          stream, p);
 }
 
 template <int D>
@@ -1173,9 +1183,8 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
     std::fprintf(stderr, "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d few=%d pieces=%d hg=%d box=%d win=(%d,%d) sinks=%d\n",
                  B, total, Hq, Hkv, d, f8, tiles, few, pieces, hg, box_rows, win_l, win_r, sinks);
   if (few) {
-    fa::fa_chunk_few_kernel<<<ctas, fa::kFewThreads, fa::FewCfg::kSmemBytes, cs>>>(
-        m[1], m[2], m[3], m[4], static_cast<const __nv_bfloat16*>(q), q_stride, p);
-    st = launch_status();
+    st = launch_dependent(fa::fa_chunk_few_kernel, dim3(ctas), fa::kFewThreads, fa::FewCfg::kSmemBytes, cs, m[1], m[2],
+                          m[3], m[4], static_cast<const __nv_bfloat16*>(q), q_stride, p);
   } else {
     st = d == 64 ? chunk_variant<64>(f8, tiles, ctas, m, p, cs) : chunk_variant<128>(f8, tiles, ctas, m, p, cs);
   }

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_write_kernel(const Cac
   constexpr int kIters = kCacheWarpElems / 256;  // 32 lanes of 8 values
   constexpr int kLanes = D / 8;                  // lanes of one row
   const Abort none{nullptr};
+  griddep_wait();  // launched as a programmatic dependent: what ran before on the stream is done
   if (blockIdx.x == 0 && blockIdx.y == 0)
     report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, threadIdx.x, kCacheThreads);
   const long long unit = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const Cach
   constexpr int kVec = kF8 ? 16 : 8;                     // values of a 16-byte piece of a page
   constexpr int kIters = kCacheWarpElems / (32 * kVec);
   const Abort none{nullptr};
+  griddep_wait();  // launched as a programmatic dependent: what ran before on the stream is done
   if (blockIdx.x == 0 && blockIdx.y == 0)
     report_bad_batch(p.cu, p.seqlens, p.B, p.total, (long long)p.max_pages * p.page_size, threadIdx.x, kCacheThreads);
   const long long unit = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);

@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
   const long long max_keys = (long long)p.max_pages * p.page_size;
 
   griddep_launch_dependents();  // the merge takes an SM as soon as its CTA is done, and waits there
+  // (Launched as a programmatic dependent itself: up to griddep_wait nothing of global memory is touched.)
   // set-up, a part per warp: barriers (a lane each), TMEM, tensor maps, and the piece of this CTA
   if (warp == 2) {
     if (lane == 0) bars->abort_flag = 0;
@@ -520,9 +521,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
     }
   } else if (warp >= 4 && warp < 8) {
     // (over the Q buffer: no load is in flight yet)
+    griddep_wait();
     chunk_plan<kTiles>(p, bars, reinterpret_cast<int*>(smem_gen), tid - 128);
     fence_proxy_async_smem();  // the Q loads may overwrite it
   }
+  griddep_wait();  // what ran before on the stream is done and visible
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;

@@ -161,9 +161,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
   } else if (warp >= 4 && warp < 8) {
     // (over the W buffers: nothing is in them yet)
+    griddep_wait();
     chunk_plan<1>(p, bars, reinterpret_cast<int*>(smem_gen + Cfg::kOffW), tid - 128);
     fence_proxy_async_smem();
   }
+  griddep_wait();  // what ran before on the stream is done and visible
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;

@@ -461,3 +461,45 @@ def test_refusals_of_the_binding():
     with pytest.raises(fa.FaError):  # K and V written to the same pages
         fa.cache_write_paged(rows, rows.clone(), t["k"], t["k"], t["table"], t["lens"], t["cu"])
     fa.check()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_calls_that_depend_on_each_other_without_a_pause(f8):
+    """Writes, attention, reads back, the decode and the plain forward one after another on a stream, each on the
+    results of the one before, give what the same calls give with the device idle between them."""
+    new, keys = [4, 4, 4], [300, 44, 1030]
+    b = Batch(new, keys, 3, 3, 128, 64, f8, seed=61, stray=0)
+    rows = [[torch.randn(b.total, 3, 128, generator=torch.Generator().manual_seed(100 + i)).bfloat16().cuda()
+             for _ in range(3)] for i in range(8)]
+
+    def run(pause):
+        t, out = b.gpu(), []
+        x = t["q"]
+        for q, k, v in rows:
+            steps = [lambda: fa.cache_write_paged(k, v, t["k"], t["v"], t["table"], t["lens"], t["cu"], t["ks"], t["vs"]),
+                     lambda: call(dict(t, q=(x + q).bfloat16()))[0],
+                     lambda: fa.cache_read_paged(t["k"], t["v"], t["table"], t["lens"], t["cu"], b.total, t["ks"], t["vs"])]
+            got = []
+            for step in steps:
+                got.append(step())
+                if pause:
+                    torch.cuda.synchronize()
+            x, (rk, rv) = got[1], got[2]
+            y, _ = fa.attention_fwd(x.view(3, 4, 3, 128), rk.view(3, 4, 3, 128), rv.view(3, 4, 3, 128), causal=True)
+            if pause:
+                torch.cuda.synchronize()
+            if not f8:
+                z, _ = fa.attention_decode_paged(y, t["k"], t["v"], t["table"], t["lens"], causal=True)
+                y = y + z
+            x = y.reshape(b.total, 3, 128)
+            if pause:
+                torch.cuda.synchronize()
+            out += [x, rk, rv]
+        torch.cuda.synchronize()
+        fa.check()
+        return out + [t["k"].view(torch.uint8), t["v"].view(torch.uint8)]
+
+    slow = run(True)
+    for _ in range(3):
+        for got, ref in zip(run(False), slow):
+            assert torch.equal(got, ref)

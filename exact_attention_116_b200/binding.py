@@ -21,9 +21,10 @@ LIB_PATH = os.path.join(_PKG, "libfa_sm100.so")
 FA_OK = 0
 STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
                 4: "FA_ERR_TIMEOUT", 5: "FA_ERR_NO_MEMORY", 6: "FA_ERR_DEVICE"}
-EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_varlen", "fa_fwd_fp8", "fa_decode_splits", "fa_decode_workspace_bytes", "fa_decode_paged",
-           "fa_cache_write", "fa_cache_read", "fa_cache_write_args", "fa_cache_read_args", "fa_chunk_workspace_bytes",
-           "fa_chunk_paged", "fa_chunk_paged_args", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_ex", "fa_bwd_varlen", "fa_bwd_deterministic", "fa_bwd_preprocess",
+EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_varlen", "fa_fwd_fp8", "fa_decode_splits", "fa_decode_workspace_bytes",
+           "fa_decode_paged", "fa_cache_write", "fa_cache_read", "fa_cache_write_args", "fa_cache_read_args", "fa_chunk_workspace_bytes",
+           "fa_chunk_paged", "fa_chunk_paged_args", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_ex", "fa_bwd_varlen",
+           "fa_bwd_deterministic", "fa_bwd_preprocess",
            "fa_bwd_main", "fa_bwd_dq_convert", "fa_bwd_static_workspace", "fa_check", "fa_status_string")
 
 _lib = None
@@ -84,8 +85,8 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_bwd_static_workspace.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i, i, vp]
     for name in ("fa_fwd", "fa_fwd_ex", "fa_bwd_ex", "fa_fwd_varlen", "fa_bwd_varlen", "fa_fwd_fp8", "fa_decode_paged",
-                 "fa_cache_write", "fa_cache_read", "fa_chunk_paged", "fa_bwd", "fa_bwd_deterministic", "fa_bwd_preprocess", "fa_bwd_main", "fa_bwd_dq_convert",
-                 "fa_bwd_static_workspace", "fa_check"):
+                 "fa_cache_write", "fa_cache_read", "fa_chunk_paged", "fa_bwd", "fa_bwd_deterministic",
+                 "fa_bwd_preprocess", "fa_bwd_main", "fa_bwd_dq_convert", "fa_bwd_static_workspace", "fa_check"):
         getattr(lib, name).restype = i
     return lib
 

@@ -1180,7 +1180,9 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   p.lse_part = reinterpret_cast<float*>(static_cast<char*>(ws) + wb.o_bytes);
   p.split = reinterpret_cast<int4*>(static_cast<char*>(ws) + wb.o_bytes + wb.lse_bytes);
   if (log_enabled())
-    std::fprintf(stderr, "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d few=%d pieces=%d hg=%d box=%d win=(%d,%d) sinks=%d\n",
+    std::fprintf(stderr,
+                 "[fa] chunk B=%d total=%d Hq=%d Hkv=%d d=%d f8=%d tiles=%d few=%d pieces=%d hg=%d box=%d win=(%d,%d) "
+                 "sinks=%d\n",
                  B, total, Hq, Hkv, d, f8, tiles, few, pieces, hg, box_rows, win_l, win_r, sinks);
   if (few) {
     st = launch_dependent(fa::fa_chunk_few_kernel, dim3(ctas), fa::kFewThreads, fa::FewCfg::kSmemBytes, cs, m[1], m[2],

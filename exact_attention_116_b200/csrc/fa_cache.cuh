@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_write_kernel(const Cac
   const int token = (int)(unit / p.parts), part = (int)(unit - (long long)token * p.parts);
   if (token >= p.total) return;
   const int width = p.H * D, first = part * kCacheWarpElems + lane * 8;
-  const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(kv ? p.rows[1] : p.rows[0]) + (long long)token * p.row_stride;
+  const __nv_bfloat16* rows =
+      static_cast<const __nv_bfloat16*>(kv ? p.rows[1] : p.rows[0]) + (long long)token * p.row_stride;
   void* cache = kv ? p.cache[1] : p.cache[0];
   uint8_t* scale = kv ? p.scale[1] : p.scale[0];
   uint4 x[kIters];

@@ -983,7 +983,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
               // two 16-byte chunks; the upper half of a row's threads stores its odd chunk first, so
               // that the eight threads of a row (d = 128) touch all banks in each store
               const uint32_t to = dst + (uint32_t)(c >> 2) * 16384u + row * 128;
-              const uint32_t a0 = to + (((2 * (c & 3) + odd) ^ (row & 7)) << 4), a1 = to + (((2 * (c & 3) + 1 - odd) ^ (row & 7)) << 4);
+              const uint32_t a0 = to + (((2 * (c & 3) + odd) ^ (row & 7)) << 4);
+              const uint32_t a1 = to + (((2 * (c & 3) + 1 - odd) ^ (row & 7)) << 4);
               st_shared_v4(a0, odd ? r[4] : r[0], odd ? r[5] : r[1], odd ? r[6] : r[2], odd ? r[7] : r[3]);
               st_shared_v4(a1, odd ? r[0] : r[4], odd ? r[1] : r[5], odd ? r[2] : r[6], odd ? r[3] : r[7]);
             }

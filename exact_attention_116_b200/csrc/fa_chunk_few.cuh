@@ -174,8 +174,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   if (warp == 0 || warp == 2) {
     // ---------------------------------------------------------------- TMA producers (all lanes): K and V
-    // (One warp took 1100 cycles to place and issue the four loads of a tile.) Lane l < 16 loads the codes of page box l of a tile, lane 16 + l its scales; boxes of keys that
-    // no row sees are filled with zeros (page num_pages), as in fa_chunk_kernel.
+    // (One warp took 1100 cycles to place and issue the four loads of a tile.) Lane l < 16 loads the
+    // codes of page box l of a tile, lane 16 + l its scales; boxes of keys that no row sees are filled
+    // with zeros (page num_pages), as in fa_chunk_kernel.
     const int groups = 128 / p.box_rows, grp = lane & 15;
     const bool loads = grp < groups, scales = lane >= 16;
     const uint32_t box_off = (uint32_t)grp * p.box_rows;
@@ -408,7 +409,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           int em = __reduce_max_sync(0xffffffffu, ev);
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) {
-            const float2 x = make_float2(warp_max_f32(fmaxf(a[0][k].x, a[1][k].x)), warp_max_f32(fmaxf(a[0][k].y, a[1][k].y)));
+            const float2 x = make_float2(warp_max_f32(fmaxf(a[0][k].x, a[1][k].x)),
+                                         warp_max_f32(fmaxf(a[0][k].y, a[1][k].y)));
             if (lane == 0) *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * k]) = x;
           }
           if (lane == 0) sE[wq] = em;

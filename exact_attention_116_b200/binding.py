@@ -632,14 +632,24 @@ def chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, l
     tensor of chunk_workspace_bytes(B, total, Hq, Hkv, d) bytes (any contents; calls that may overlap need
     workspaces of their own), or None to allocate one."""
     index = _cuda_index(q)
-    B, Hkv, d, num_pages, page_size, max_pages, ks, vs = _check_cache(index, k_cache, v_cache, k_scale, v_scale,
-                                                                      block_table, seqlens, cu_seqlens)
-    stride = _check_rows(q, "q", index, None, d)
+    plan = _check_cache(index, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens)
+    stride = _check_rows(q, "q", index, None, plan[2])
     total, Hq, _ = q.shape
     if o.shape != q.shape or o.dtype != torch.bfloat16 or o.get_device() != index or not o.is_contiguous():
         raise ValueError("o must be a contiguous bfloat16 tensor of q's shape on its device")
     if lse.shape != (Hq, total) or lse.dtype != torch.float32 or lse.get_device() != index or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous ({Hq}, {total}) float32 tensor on q's device")
+    if workspace is not None and workspace.get_device() != index:
+        raise ValueError("workspace must be on q's device")
+    _chunk(index, q, stride, k_cache, v_cache, block_table, seqlens, cu_seqlens, plan, o, lse, scale, causal, window,
+           sinks, workspace, stream)
+
+
+def _chunk(index, q, stride, k_cache, v_cache, block_table, seqlens, cu_seqlens, plan, o, lse, scale, causal, window,
+           sinks, workspace, stream) -> None:
+    """fa_chunk_paged with checked tensors; plan: what _check_cache returned."""
+    B, Hkv, d, num_pages, page_size, max_pages, ks, vs = plan
+    total, Hq, _ = q.shape
     if Hq == 0 or Hkv == 0 or Hq % Hkv:
         raise ValueError(f"the {Hq} query heads must be a multiple of the cache's {Hkv}")
     if workspace is None:
@@ -651,8 +661,6 @@ def chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, l
                 workspace = torch.empty_strided((wb,), (1,), dtype=torch.uint8, device=q.device)
         ws = workspace.data_ptr()
     else:
-        if workspace.get_device() != index:
-            raise ValueError("workspace must be on q's device")
         ws, wb = _check_workspace(workspace)
     _launch("fa_chunk_paged", index, _CHUNK_ARGS.pack(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(), seqlens.data_ptr(),
@@ -670,15 +678,16 @@ def attention_chunk_paged(q, k_cache, v_cache, block_table, seqlens, cu_seqlens,
     seqlens[b] keys; query head h reads cache head h // (Hq // Hkv). Pages and scales as in cache_write_paged.
     ``window``: (left, right) as everywhere; ``sinks``: a sequence's first keys that stay visible left of the
     window. Rows from cu_seqlens[B] on are not initialised (chunk_paged_into leaves them as they were)."""
-    if q.dim() != 3:
-        raise ValueError("q must be a (total, heads, head_dim) bfloat16 CUDA tensor")
+    index = _cuda_index(q)
+    plan = _check_cache(index, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens)
+    stride = _check_rows(q, "q", index, None, plan[2])
     total, Hq, _ = q.shape
 
     def make():
         return (torch.empty_like(q, memory_format=torch.contiguous_format),
                 torch.empty_strided((Hq, total), (max(total, 1), 1), dtype=torch.float32, device=q.device))
 
-    o, lse = _outputs_on(stream, q.device, make)
-    chunk_paged_into(q, k_cache, v_cache, block_table, seqlens, cu_seqlens, o, lse, scale, causal, window, sinks,
-                     k_scale, v_scale, None, stream)
+    o, lse = make() if stream is None else _outputs_on(stream, q.device, make)
+    _chunk(index, q, stride, k_cache, v_cache, block_table, seqlens, cu_seqlens, plan, o, lse, scale, causal, window,
+           sinks, None, stream)
     return o, lse

@@ -894,7 +894,8 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, const float* q_desca
 namespace {
 
 // The decode kernel, compiled for up to 4 or up to 8 new rows, launched as the programmatic
-// dependent of the kernel before it on the stream (the prep kernel, when there are splits).
+// dependent of the kernel before it on the stream: the prep kernel, which follows all that came
+// before in full, or with one piece whatever the caller launched last (the kernel then waits for it).
 template <int D>
 int launch_decode(dim3 grid, const CUtensorMap& mk, const CUtensorMap& mv, const fa::DecParams& p,
                   cudaStream_t cs) {

@@ -66,8 +66,9 @@ __device__ __forceinline__ int cache_place(const CacheParams& p, int token, int&
   const int b = seg_of(p.cu, p.B, token);
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), n = __ldg(p.seqlens + b);
   if (token < c0 || token >= c1 || c0 < 0 || c1 > p.total) return -1;
+  if (n < 0 || n > (long long)p.max_pages * p.page_size) return 0;  // (a length near -2^31 would wrap below)
   const int pos = n - (c1 - c0) + (token - c0);
-  if (pos < 0 || n > (long long)p.max_pages * p.page_size) return 0;
+  if (pos < 0) return 0;
   page = __ldg(p.block_table + (size_t)b * p.max_pages + pos / p.page_size);
   row = pos % p.page_size;
   if (page < 0 || page >= p.num_pages) {

@@ -9,11 +9,10 @@
 //   score(row, key) = S * 2^ek * scale,   W(row, key) = P(row, key) * 2^(ev - E).
 // Q and W are sums of three E5M2 numbers, each the remainder of the ones before rounded to 3
 // significant bits: bf16 queries (8 bits) exactly, weights to 9 bits (bf16 keeps 8), with the range
-// of E5M2 below the largest: a query's elements down to 2^-31 of its row's largest, weights down to
-// 2^-27 of the row's reference. Products of E4M3 and E5M2 codes are exact, sums are fp32. The three
-// terms of Q go into one accumulator, those of W are 3 x 16 columns of one product (V is read
-// once). E is the largest ev so far; a value 2^20 times smaller than the sequence's largest has
-// weights of 7 bits and fewer.
+// of E5M2 below the largest: a query's elements down to 2^-31 of its row's largest, W down to 2^-26 of
+// the row's largest and its 9 bits down to 2^-17 of it. Products of E4M3 and E5M2 codes are exact, sums
+// are fp32. The three terms of Q go into one accumulator, those of W are 3 x 16 columns of one product
+// (V is read once).
 //
 // Against bf16 operand tiles made from the codes (fa_chunk.cuh): no conversion, which took 2.4 us a
 // tile of 128 keys on one SM, and half the shared-memory traffic. Bound by HBM: 33 KB a tile in
@@ -23,9 +22,15 @@
 // the number of row pairs 153. With 16 rows a pair of tiles takes 4500 cycles, all in the softmax.
 //
 // Per tile a thread handles one key: x = score - the row's reference m (log2), P = 2^x rounded to 9
-// bits, summed before (log-sum-exp) and after the rounding (divisor of O). The references move only
-// when some x exceeds 4 or some ev exceeds E + 1, which one barrier's vote tells; then the exact
-// maxima are taken and O is rescaled. W <= 2^(4 + 1 + 10), E5M2 ends at 1.75 * 2^15.
+// bits, summed before (log-sum-exp) and after the rounding (divisor of O). E is fixed at the block's first
+// keys (their largest ev, within [-14, 24]), and m is the row's largest score + ev, less E: so every row's
+// largest W is near 2^10, whatever the values are that other rows see or that it gives no weight. (With m
+// from the scores alone and E the block's largest ev, a key with values 2^28 times larger that one of the
+// rows sees took all bits from the weights of the others.) P itself is then about 2^(E - ev), in fp32's
+// range with 2^-26 to spare below for ev from E - 96 to E + 100. Where a block's values differ by more, a
+// row of the smaller ones loses bits (m is held to the scores' maximum less 96) and so does one of the
+// larger. The references move only when some x + ev exceeds E + 5, which one barrier's vote tells; then
+// the exact maxima are taken and O is rescaled. W <= 2^(5 + 10), E5M2 ends at 1.75 * 2^15.
 //
 // Warps: 0 loads; 1 issues MMAs; 4-7 softmax and epilogue (and the set-up); 8-11 split the next
 // block's queries, ahead.
@@ -39,8 +44,10 @@ constexpr int kFewRows = 16, kFewTerms = 3, kFewSlots = 5;
 constexpr int kFewBufs = 4;        // tiles of scores and of weights in flight: two pairs
 constexpr int kFewThreads = 384;
 constexpr int kFewD = 128;
-constexpr float kFewGrow = 4.0f;   // log2: how far a score may exceed its row's reference
+constexpr float kFewGrow = 5.0f;   // log2: how far P * 2^ev may exceed 2^E
 constexpr int kFewShift = 10;      // W = P * 2^(ev - E + 10)
+constexpr int kFewLeastE = -14, kFewMostE = 24, kFewNoE = -1000;  // (-1000: not fixed yet)
+constexpr int kFewSpan = 96;       // P <= 2^(96 + 5): sums of 2^26 of them stay in fp32's range
 
 struct FewCfg {
   static constexpr int kSlotBytes = 128 * kFewD + 1024;  // codes, then the scales of each page box at 128 bytes
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars->q_empty[qb]));
-      int E = -1000;
+      int E = kFewNoE;
       uint32_t unset = (1u << rows) - 1u;  // rows that have seen no key: their reference is not one yet
 
       // Two tiles at a time: this thread has key key_in of each. (One at a time took 1900 cycles a tile,
@@ -372,9 +379,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
         // scores against the references, -inf where masked; is the key seen at all?
         float2 a[2][kPairs];
-        bool seen[2];
-        float most = -INFINITY;
-        int ev = -1000;
+        bool seen[2], over = unset != 0 || E == kFewNoE;
+        int ev[2];  // less E, at least -96 (a key without values: -96)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const float kf = ks[u] == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000)
@@ -400,24 +406,35 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if (!vis) (e ? a[u][k].y : a[u][k].x) = -INFINITY;
               }
           }
+          float most = -INFINITY;
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) most = max3(most, a[u][k].x, a[u][k].y);
-          if (seen[u] && vs[u] != (uint32_t)kScaleNan) ev = max(ev, (int)vs[u] - 127);
+          const bool has = seen[u] && vs[u] != (uint32_t)kScaleNan;
+          ev[u] = has ? max((int)vs[u] - 127 - E, -kFewSpan) : -kFewSpan;
+          over |= most + (float)ev[u] > kFewGrow;
         }
-        if (few_vote(most > kFewGrow || ev > E + 1 || unset != 0)) {
-          // exact maxima over the tiles' keys; the sums and O follow the new references
-          int em = __reduce_max_sync(0xffffffffu, ev);
+        if (few_vote(over)) {
+          if (E == kFewNoE) {  // the first keys with values fix it
+            const int em = __reduce_max_sync(0xffffffffu, max(ev[0], ev[1]));
+            if (lane == 0) sE[wq] = em;
+            named_bar_sync(2, 128);
+            const int most_ev = max(max(sE[0], sE[1]), max(sE[2], sE[3])) + kFewNoE;
+            if (most_ev > kFewNoE - kFewSpan) {
+              E = min(max(most_ev, kFewLeastE), kFewMostE);
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                if (ev[u] > -kFewSpan) ev[u] = max(ev[u] + kFewNoE - E, -kFewSpan);
+            }
+          }
+          // exact maxima over the tiles' keys of x + ev - E; the sums and O follow the new references
+          const float2 ev0 = make_float2((float)ev[0], (float)ev[0]), ev1 = make_float2((float)ev[1], (float)ev[1]);
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) {
-            const float2 x = make_float2(warp_max_f32(fmaxf(a[0][k].x, a[1][k].x)),
-                                         warp_max_f32(fmaxf(a[0][k].y, a[1][k].y)));
+            const float2 y0 = add2(a[0][k], ev0), y1 = add2(a[1][k], ev1);
+            const float2 x = make_float2(warp_max_f32(fmaxf(y0.x, y1.x)), warp_max_f32(fmaxf(y0.y, y1.y)));
             if (lane == 0) *reinterpret_cast<float2*>(&sX[wq * kFewRows + 2 * k]) = x;
           }
-          if (lane == 0) sE[wq] = em;
           named_bar_sync(2, 128);
-          em = max(max(sE[0], sE[1]), max(sE[2], sE[3]));
-          const int e_new = max(E, em);
-          const float e_step = E <= -1000 ? 0.0f : exp2_int(E - e_new);
           float2 alpha[kPairs];
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) {
@@ -442,7 +459,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             l2[k] = mul2(l2[k], alpha[k]);
             lr2[k] = mul2(lr2[k], alpha[k]);
           }
-          E = e_new;
           if (v > 0) {
             pv_wait(n - 1);
 #pragma unroll
@@ -456,8 +472,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   if (hf * 4 + k >= kPairs) continue;
-                  o[2 * k] = __float_as_uint(__uint_as_float(o[2 * k]) * (alpha[hf * 4 + k].x * e_step));
-                  o[2 * k + 1] = __float_as_uint(__uint_as_float(o[2 * k + 1]) * (alpha[hf * 4 + k].y * e_step));
+                  o[2 * k] = __float_as_uint(__uint_as_float(o[2 * k]) * alpha[hf * 4 + k].x);
+                  o[2 * k + 1] = __float_as_uint(__uint_as_float(o[2 * k + 1]) * alpha[hf * 4 + k].y);
                 }
                 tmem_st8(at, o);
               }
@@ -471,7 +487,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int u = 0; u < 2; ++u)
           vf[u] = !seen[u]                        ? 0.0f
                   : vs[u] == (uint32_t)kScaleNan ? __int_as_float(0x7fc00000)
-                                                 : exp2_int((int)vs[u] - 127 - E + kFewShift);
+                                                 : exp2_int(min((int)vs[u] - 127 - E + kFewShift, 127));
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
           uint32_t t[2][kFewTerms];
@@ -526,7 +542,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       named_bar_sync(2, 128);
       pv_wait(n - 1);
-      const float e_unit = exp2_int(max(E, -110) - kFewShift);
+      const float e_unit = exp2_int(E - kFewShift);
       const long long o_size = (long long)p.total * p.Hq * D, part_rows = 2LL * p.ctas * 128;
 #pragma unroll
       for (int hf = 0; hf < (kPairs > 4 ? 2 : 1); ++hf) {

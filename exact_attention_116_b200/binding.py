@@ -485,8 +485,9 @@ def _check_rows(t: torch.Tensor, name: str, index: int, heads: int | None, d: in
     return s0
 
 
-_E4M3 = (torch.float8_e4m3fn, torch.uint8)
-_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+# (a torch without one of these types has the bytes as uint8)
+_E4M3 = tuple(t for t in (getattr(torch, "float8_e4m3fn", None), torch.uint8) if t is not None)
+_E8M0 = tuple(t for t in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if t is not None)
 
 
 def _check_cache(index: int, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens):

@@ -34,6 +34,7 @@ std::mutex g_mu;
 EncodeTiledFn g_encode = nullptr;
 int g_sm_count[kMaxDevices] = {0};
 bool g_attr_done[kMaxDevices] = {false};
+bool g_chunk_done[kMaxDevices] = {false};
 bool g_is_sm100[kMaxDevices] = {false};
 
 EncodeTiledFn encode_fn() {
@@ -97,9 +98,7 @@ bool chunk_attribute() {
 
 template <int D>
 bool chunk_attributes() {
-  return cudaFuncSetAttribute(fa::fa_chunk_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              fa::FewCfg::kSmemBytes) == cudaSuccess &&
-         chunk_attribute<D, false, 1>() && chunk_attribute<D, false, 2>() && chunk_attribute<D, true, 1>() &&
+  return chunk_attribute<D, false, 1>() && chunk_attribute<D, false, 2>() && chunk_attribute<D, true, 1>() &&
          chunk_attribute<D, true, 2>();
 }
 
@@ -118,8 +117,7 @@ int device_setup(int* dev_out, int* sm_count) {
     if (g_is_sm100[dev]) {
       if (cudaFuncSetAttribute(fa::fa_fwd_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                fa::FwdCfg<128, true>::kSmemBytes) != cudaSuccess ||
-          !decode_attributes<64>() || !decode_attributes<128>() || !chunk_attributes<64>() ||
-          !chunk_attributes<128>() ||
+          !decode_attributes<64>() || !decode_attributes<128>() ||
           !bwd_attributes<64>() || !bwd_attributes<128>())
         return FA_ERR_CUDA;
     }
@@ -128,6 +126,22 @@ int device_setup(int* dev_out, int* sm_count) {
   if (!g_is_sm100[dev]) return FA_ERR_UNSUPPORTED;
   *dev_out = dev;
   *sm_count = g_sm_count[dev];
+  return FA_OK;
+}
+
+// The same for the chunk kernels, at the first call that needs them: setting an attribute loads its kernel,
+// 0.5 ms for these nine. (A process's first forward takes 19.0 ms of set-up with them here, 19.5 with them
+// above, and 14.4 in a library without the paged calls, whose module is a quarter smaller.)
+int chunk_setup(int* dev, int* sm_count) {
+  const int st = device_setup(dev, sm_count);
+  if (st) return st;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_chunk_done[*dev]) return FA_OK;
+  if (cudaFuncSetAttribute(fa::fa_chunk_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           fa::FewCfg::kSmemBytes) != cudaSuccess ||
+      !chunk_attributes<64>() || !chunk_attributes<128>())
+    return FA_ERR_CUDA;
+  g_chunk_done[*dev] = true;
   return FA_OK;
 }
 
@@ -1091,7 +1105,7 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const void* k_scale,
 size_t fa_chunk_workspace_bytes(int B, int total, int Hq, int Hkv, int d) {
   if (B < 1 || total < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
   int dev, sms;
-  if (device_setup(&dev, &sms)) return 0;
+  if (chunk_setup(&dev, &sms)) return 0;
   return chunk_workspace(sms, chunk_tiles(B, total, Hq / Hkv), d).bytes();
 }
 
@@ -1125,7 +1139,7 @@ int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const
   if (any_overlap({o, ob}, ins, 8) || any_overlap({lse, lb}, ins, 8) || (o && lse && overlap(o, ob, lse, lb)))
     return FA_ERR_INVALID_ARG;
   int dev, sms;
-  if ((st = device_setup(&dev, &sms))) return st;
+  if ((st = chunk_setup(&dev, &sms))) return st;
   if (total == 0) return FA_OK;
   const bool few = chunk_few(f8, d, B, total, G);
   const int tiles = chunk_tiles(B, total, G), tq = (few ? fa::kFewRows : 128) / G;

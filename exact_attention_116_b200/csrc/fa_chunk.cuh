@@ -769,8 +769,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         const bool all = pos_lo >= 0 && k1 < w.n && (p.win_r < 0 || k1 <= pos_lo + p.win_r) &&
                          (p.win_l < 0 || key0 >= pos_hi - p.win_l || k1 < p.sinks);
         bool none = false;  // no score of this warp is visible
+        uint32_t m[2] = {~0u, ~0u};
         if (!all) {
-          uint32_t m[2];
           chunk_visible(kbase, kmin, kmax, p.sinks, m);
           none = __all_sync(0xffffffffu, (m[0] | m[1]) == 0u);
           if (!none && !__all_sync(0xffffffffu, (m[0] & m[1]) == ~0u)) {
@@ -782,10 +782,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
         if (!none) {
           if (pos_scale) {
             m_tile = fwd_tile_max<true>(x, false, 0, 0, 0, c);
-          } else {  // masked scores stay -inf whatever the scale's sign
+          } else {  // masked scores stay -inf whatever the scale's sign (a visible -inf does not)
 #pragma unroll
             for (int cc = 0; cc < kC; ++cc) {
-              x[cc] = x[cc] == -INFINITY && !all ? -INFINITY : x[cc] * c;
+              x[cc] = (m[cc >> 5] >> (cc & 31)) & 1u ? x[cc] * c : -INFINITY;
               m_tile = fmaxf(m_tile, x[cc]);
             }
           }

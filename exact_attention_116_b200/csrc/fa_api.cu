@@ -589,7 +589,7 @@ bool rows_overlap(const void* a, const void* b, int total, size_t width, long lo
 
 // A launch that may begin while the kernel before it on the stream ends (its kernels wait for that one
 // before they touch global memory, in every thread, so that the end of one implies the end of those
-// before it). It saves 2 us a call: a step over bf16 pages 76.9 -> 74.6 us, a read of 609 MB 98.8 -> 96.5.
+// before it; so does the decode kernel, or its prep kernel). It saves 2 us a call: a step over bf16 pages 76.9 -> 74.6 us, a read of 609 MB 98.8 -> 96.5.
 template <class... Params, class... Args>
 int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
@@ -715,9 +715,15 @@ int make_map_scales(CUtensorMap* m, const void* base, int num_pages, int page_si
 }
 
 // One or two 128-row tiles per block of the chunk kernel: two share every K/V load, which long chunks
-// need; with few rows to a sequence the second would stand idle. Measured with one / two (us, bf16
-// pages, 8 sequences): 1 row over 6000 keys 74.6 / 78.8; over 4000 keys 64 rows 41.6 / 41.5, 128 rows
-// 47.0 / 43.8, 256 rows 70.5 / 55.6; two chunks of 1024 tokens x 4 heads 170 / 130.
+// need; with few rows to a sequence the second would stand idle. Measured with one / two (us in a graph, 8
+// sequences of 4000 keys, 32 query heads over 8), by rows of a sequence:
+//                    4           32          64          96          128         256
+//   bf16, d = 128   33.6/35.7   36.6/37.3   38.6/38.7   41.3/39.9   44.0/40.5   66.1/51.5
+//   E4M3, d = 128               42.0/42.2   43.6/43.5   45.8/44.8   48.9/46.3   80.3/62.7
+//   bf16, d = 64    28.4/31.1   31.1/32.9   32.7/33.3   33.6/33.8   35.5/34.3   58.2/45.0
+//   E4M3, d = 64    33.5/34.6   35.9/36.5   36.6/37.0   37.5/37.3   39.3/37.9   64.8/46.9
+// The rows are the batch's average (the lengths are on the device): among 255 steps, a chunk of 1000 tokens
+// takes 820 / 1121 with all contexts 4K (bf16, d = 128), 1037 / 761 with 32K under the chunk and 1K else.
 int chunk_tiles(int B, int total, int G) { return (double)total * G <= 64.0 * B ? 1 : 2; }
 
 // Heads whose CTAs run next to each other: the most of 4, 2 and 1 that divides the heads and the SMs.
@@ -731,9 +737,13 @@ int chunk_head_group(int Hkv, int sms) {
 }
 
 // Rows of a few tokens over E4M3 pages take the transposed kernel: when a sequence's rows fit its
-// 16-row blocks on average (a longer chunk in such a batch is cut into several, which read its keys
-// again). A step of 48 sequences of 2000 to 15630 keys, 4 query heads to each of 8: 153 us, 450 with
-// fa_chunk_kernel.
+// 16-row blocks on average (the lengths are on the device; padded rows count). Measured with it / with
+// fa_chunk_kernel (us in a graph): a step of 48 sequences of 2000 to 15630 keys, 4 query heads to each of 8,
+// 1 token 148 / 367, 3 tokens 216 / 368, 4 tokens 225 / 368; 16 heads to each of 4 136 / 191; 16 sequences,
+// a head each of 16, 74 / 181. A longer chunk in such a batch is cut into several blocks, which read its
+// keys again: a chunk of 20 tokens among 63 steps, all over 4K keys, 171 / 233, one of 512 among 199 over 8K
+// 1171 / 1469, but one of 512 over 32K among 199 steps over 1K 1569 / 681 (in two calls: 333 and 90), one
+// of 16 over 64K among 15 over 300, 8 heads to each of 8, 313 / 92 (in two: 77 and 21).
 bool chunk_few(bool f8, int d, int B, int total, int G) {
   return f8 && d == fa::kFewD && G <= fa::kFewRows && (double)total <= (double)B * (fa::kFewRows / G);
 }

@@ -16,10 +16,12 @@
 //
 // Against bf16 operand tiles made from the codes (fa_chunk.cuh): no conversion, which took 2.4 us a
 // tile of 128 keys on one SM, and half the shared-memory traffic. Bound by HBM: 33 KB a tile in
-// 0.82 us, 6.0 TB/s in all; a step of 48 sequences (873 MB) in 153 us, 135 at the copy rate. How it got
+// 0.82 us, 6.0 TB/s in all; a step of 48 sequences (873 MB) in 148 to 150 us, 135 at the copy rate. How it got
 // there: one tile at a time 218 us, 128- or 256-byte reads of neighbouring heads at about the same
 // time 207, all waits of a step ahead of its loads 184, a lane per wait and straight-line code for
-// the number of row pairs 153. With 16 rows a pair of tiles takes 4500 cycles, all in the softmax.
+// the number of row pairs 153, one reference per row for scores and values 150 (16 rows: 240 to 230;
+// with a second reference for each row's values 286). With 16 rows a pair of tiles takes 4500 cycles, all
+// in the softmax.
 //
 // Per tile a thread handles one key: x = score - the row's reference m (log2), P = 2^x rounded to 9
 // bits, summed before (log-sum-exp) and after the rounding (divisor of O). E is fixed at the block's first

@@ -237,7 +237,8 @@ size_t fa_chunk_workspace_bytes(int B, int total, int Hq, int Hkv, int d);
  * 2^96 of each other, beyond which rows lose bits). Workspace of
  * fa_chunk_workspace_bytes (256-byte aligned, any contents), or NULL to allocate on `stream`; calls
  * that may overlap need workspaces of their own. Results do not depend on the order in which
- * CTAs run. One or two launches on `stream`.
+ * CTAs run. One or two launches on `stream`. One kernel serves the batch, picked by the average rows
+ * of a sequence: single steps over short contexts beside a chunk over a long one are better two calls.
  */
 int fa_chunk_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const void* k_scale,
                    const void* v_scale, const int* block_table, const int* seqlens, const int* cu_seqlens, void* o,

@@ -64,12 +64,12 @@ __device__ __forceinline__ void report_bad_batch(const int* cu, const int* seqle
 // negative or its length or page out of range), -1 for a row of no sequence.
 __device__ __forceinline__ int cache_place(const CacheParams& p, int token, int& page, int& row) {
   const int b = seg_of(p.cu, p.B, token);
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), n = __ldg(p.seqlens + b);
+  const int c0 = p.cu[b], c1 = p.cu[b + 1], n = p.seqlens[b];
   if (token < c0 || token >= c1 || c0 < 0 || c1 > p.total) return -1;
   if (n < 0 || n > (long long)p.max_pages * p.page_size) return 0;  // (a length near -2^31 would wrap below)
   const int pos = n - (c1 - c0) + (token - c0);
   if (pos < 0) return 0;
-  page = __ldg(p.block_table + (size_t)b * p.max_pages + pos / p.page_size);
+  page = p.block_table[(size_t)b * p.max_pages + pos / p.page_size];
   row = pos % p.page_size;
   if (page < 0 || page >= p.num_pages) {
     atomicOr(&g_fa_error, kErrBadInput);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_write_kernel(const Cac
   for (int i = 0; i < kIters; ++i) {
     const int at = first + i * 256;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (at < width) x[i] = __ldcs(reinterpret_cast<const uint4*>(rows + at));
+    if (at < width) x[i] = ld_global_cs(rows + at);
   }
   int page = 0, row = 0;
   if (cache_place(p, token, page, row) <= 0) return;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const Cach
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     s[i] = kScaleMin;
     if (placed && at < width && dbg_range(none, base + at, kVec, size)) {
-      x[i] = __ldcs(reinterpret_cast<const uint4*>(cache + (base + at) * (kF8 ? 1 : 2)));
+      x[i] = ld_global_cs(cache + (base + at) * (kF8 ? 1 : 2));
       if (kF8) s[i] = scale[((long long)page * p.H + at / D) * p.page_size + row];
     }
   }

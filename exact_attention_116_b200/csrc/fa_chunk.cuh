@@ -126,8 +126,8 @@ struct ChunkSeq {
 };
 __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b) {
   ChunkSeq s;
-  s.c0 = __ldg(p.cu + b);
-  const int c1 = __ldg(p.cu + b + 1), n = __ldg(p.seqlens + b);
+  s.c0 = p.cu[b];
+  const int c1 = p.cu[b + 1], n = p.seqlens[b];
   s.rows = (s.c0 < 0 || c1 < s.c0 || c1 > p.total) ? 0 : c1 - s.c0;
   s.n = (n < 0 || n > (long long)p.max_pages * p.page_size) ? 0 : n;
   return s;
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kF8, kTiles>::kThreads, 1)
       const int in_seq = p.by_page(key);
       const long long ti = (long long)w.b * p.max_pages + in_seq;
       if (!dbg_range(ab, ti, 1, (long long)p.B * p.max_pages)) return;
-      page = __ldg(p.block_table + ti);
+      page = p.block_table[ti];
       row = key - in_seq * p.page_size;
     };
     int page = 0, row = 0;
@@ -1023,7 +1023,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const Chu
   const Abort none{nullptr};
   griddep_wait();  // the pieces have been written
   const int pf = blockIdx.x;
-  const int4 s = __ldcg(p.split + pf);
+  const int4 s = p.split[pf];
   const int m = (s.w >> 1) + 1, first = blockIdx.y * kMergeRows, nrows = min(kMergeRows, s.y * p.G - first);
   if (nrows <= 0 || !dbg_range(none, pf, (m - 1) * p.hg + 1, p.ctas)) return;
   // a warp's threads: rows side by side (their number rounded up to a power of two), then columns
@@ -1043,8 +1043,8 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk_merge_kernel(const Chu
         o4[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (from + i >= m) continue;
         const long long tile = (2LL * (pf + (from + i) * p.hg) + (from + i == 0 ? (s.w & 1) : 0)) * kTiles + t;
-        lse[i] = __ldcg(p.lse_part + tile * 128 + srow);
-        o4[i] = __ldcg(reinterpret_cast<const float4*>(p.o_part + tile * 128 * D) + c4 * 128 + srow);
+        lse[i] = ld_global_cg(p.lse_part + tile * 128 + srow);
+        o4[i] = ld_global_cg(reinterpret_cast<const float4*>(p.o_part + tile * 128 * D) + c4 * 128 + srow);
       }
       float most = mx;
 #pragma unroll

@@ -126,7 +126,7 @@ __device__ __forceinline__ float exp2_int(int e) { return e < -126 ? 0.0f : __in
 __global__ void __launch_bounds__(kFewThreads, 1)
     fa_chunk_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
-                        const __nv_bfloat16* __restrict__ q, long long q_stride, const ChunkParams p) {
+                        const __nv_bfloat16* q, long long q_stride, const ChunkParams p) {
   using Cfg = FewCfg;
   constexpr int D = kFewD;
   static_assert(sizeof(FewBars) <= 1536, "barrier block");
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const int in_seq = p.by_page(key);
         const long long ti = (long long)w.b * p.max_pages + in_seq;
         if (!dbg_range(ab, ti, 1, (long long)p.B * p.max_pages)) return;
-        page = __ldg(p.block_table + ti);
+        page = p.block_table[ti];
         row = key - in_seq * p.page_size;
       };
       int page = 0, row = 0;
@@ -620,8 +620,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const long long qi = ((long long)w.c0 + itok) * q_stride + (long long)head * D + c * 16;
       uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
       if (row < w.ntok * p.G) {
-        x[0] = __ldg(reinterpret_cast<const uint4*>(q + qi));
-        x[1] = __ldg(reinterpret_cast<const uint4*>(q + qi + 8));
+        x[0] = *reinterpret_cast<const uint4*>(q + qi);
+        x[1] = *reinterpret_cast<const uint4*>(q + qi + 8);
       }
       const uint32_t in[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
       uint32_t most = 0;

@@ -31,7 +31,7 @@ __device__ __forceinline__ int seg_of(const int* cu, int nseg, int row) {
   int lo = 0, hi = nseg - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu + mid) <= row) lo = mid;
+    if (cu[mid] <= row) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -529,5 +529,25 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Loads with a cache hint that keep their place behind the wait (what another kernel writes while this one
+// has already begun is not constant: no ld.global.nc for it, and no load that the compiler may move).
+__device__ __forceinline__ uint4 ld_global_cs(const void* p) {  // read once
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ld_global_cg(const float4* p) {  // from L2
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_global_cg(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
 
 }  // namespace fa

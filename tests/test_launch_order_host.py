@@ -56,3 +56,13 @@ def test_the_decode_kernel_waits_in_every_thread_and_for_its_prep_kernel():
     assert re.search(r";\s*if \(p\.pieces == 1\) griddep_wait\(\);", text[:prologue])
     end = text.rindex("__syncthreads()")
     assert re.search(r"if \(tid == 0\) griddep_wait\(\);\s*$", text[:end])  # outside every role's branch
+
+
+@pytest.mark.parametrize("name", ["fa_cache.cuh", "fa_chunk.cuh", "fa_chunk_few.cuh"])
+def test_nothing_is_read_as_constant(name):
+    """These kernels live while the one before them still writes: no load may be one of memory that stays as it
+    is for the kernel's life (which may also be moved ahead of the wait)."""
+    text = source(name)
+    assert not re.findall(r"__ld(?:g|cs|cg|ca|lu|cv)\(|__restrict__", text)
+    seg_of = source("sm100_ptx.cuh")
+    assert "__ldg" not in seg_of[seg_of.index("int seg_of("):seg_of.index("void seg_bounds(")]

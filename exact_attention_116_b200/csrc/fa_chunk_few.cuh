@@ -29,9 +29,9 @@
 // largest W is near 2^10, whatever the values are that other rows see or that it gives no weight. (With m
 // from the scores alone and E the block's largest ev, a key with values 2^28 times larger that one of the
 // rows sees took all bits from the weights of the others.) P itself is then about 2^(E - ev), in fp32's
-// range with 2^-26 to spare below for ev from E - 96 to E + 100. Where a block's values differ by more, a
-// row of the smaller ones loses bits (m is held to the scores' maximum less 96) and so does one of the
-// larger. The references move only when some x + ev exceeds E + 5, which one barrier's vote tells; then
+// range with 2^-26 to spare below for ev from E - 96 to E + 100. Where a block's values differ by more, m is
+// held to the scores' maximum less 96 and plus 100: O loses bits, or its largest weights end at E5M2's
+// largest number, and the log-sum-exp stands. The references move only when some x + ev exceeds E + 5, which one barrier's vote tells; then
 // the exact maxima are taken and O is rescaled. W <= 2^(5 + 10), E5M2 ends at 1.75 * 2^15.
 //
 // Warps: 0 loads; 1 issues MMAs; 4-7 softmax and epilogue (and the set-up); 8-11 split the next
@@ -50,6 +50,7 @@ constexpr float kFewGrow = 5.0f;   // log2: how far P * 2^ev may exceed 2^E
 constexpr int kFewShift = 10;      // W = P * 2^(ev - E + 10)
 constexpr int kFewLeastE = -14, kFewMostE = 24, kFewNoE = -1000;  // (-1000: not fixed yet)
 constexpr int kFewSpan = 96;       // P <= 2^(96 + 5): sums of 2^26 of them stay in fp32's range
+constexpr int kFewRise = 100;      // and a row's largest P >= 2^-100
 
 struct FewCfg {
   static constexpr int kSlotBytes = 128 * kFewD + 1024;  // codes, then the scales of each page box at 128 bytes
@@ -428,8 +429,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if (ev[u] > -kFewSpan) ev[u] = max(ev[u] + kFewNoE - E, -kFewSpan);
             }
           }
-          // exact maxima over the tiles' keys of x + ev - E; the sums and O follow the new references
-          const float2 ev0 = make_float2((float)ev[0], (float)ev[0]), ev1 = make_float2((float)ev[1], (float)ev[1]);
+          // exact maxima over the tiles' keys of x + ev - E; the sums and O follow the new references (P of the
+          // largest score stays above 2^-100: the log-sum-exp stands whatever the values are)
+          const float ev_0 = (float)min(ev[0], kFewRise), ev_1 = (float)min(ev[1], kFewRise);
+          const float2 ev0 = make_float2(ev_0, ev_0), ev1 = make_float2(ev_1, ev_1);
 #pragma unroll
           for (int k = 0; k < kPairs; ++k) {
             const float2 y0 = add2(a[0][k], ev0), y1 = add2(a[1][k], ev1);
@@ -458,8 +461,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             m2[k] = add2(m2[k], up);
             a[0][k] = sub2(a[0][k], up);
             a[1][k] = sub2(a[1][k], up);
-            l2[k] = mul2(l2[k], alpha[k]);
-            lr2[k] = mul2(lr2[k], alpha[k]);
+            float2 fall = alpha[k];
+            if (fmaxf(up.x, up.y) > 120.0f) {  // the sums may fall from 2^96 to 2^-100: a factor beyond fp32, in halves
+              fall = make_float2(fminf(ex2_approx(-0.5f * up.x), 1.0f), fminf(ex2_approx(-0.5f * up.y), 1.0f));
+              l2[k] = mul2(l2[k], fall);
+              lr2[k] = mul2(lr2[k], fall);
+            }
+            l2[k] = mul2(l2[k], fall);
+            lr2[k] = mul2(lr2[k], fall);
           }
           if (v > 0) {
             pv_wait(n - 1);

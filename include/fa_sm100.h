@@ -234,7 +234,7 @@ size_t fa_chunk_workspace_bytes(int B, int total, int Hq, int Hkv, int d);
  * `sinks` keys stay visible left of the window. Masked scores carry no weight whatever K holds
  * there; V rows that some row of the same 128- or 256-row block sees must be finite (over E4M3 pages
  * with d = 128 and few rows to a sequence: of the same 16-row block, and their scales should lie within
- * 2^96 of each other, beyond which rows lose bits). Workspace of
+ * 2^96 of each other, beyond which O loses bits). Workspace of
  * fa_chunk_workspace_bytes (256-byte aligned, any contents), or NULL to allocate on `stream`; calls
  * that may overlap need workspaces of their own. Results do not depend on the order in which
  * CTAs run. One or two launches on `stream`. One kernel serves the batch, picked by the average rows

@@ -166,3 +166,23 @@ def test_values_of_zero_leave_the_log_sum_exp():
     check(b, what="zeros under different scales")
     b.v.view(torch.uint8)[int(b.table[0, 20])] = 0x30  # 0.5: a page of values in the first sequence
     check(b, what="zeros and values")
+
+
+@pytest.mark.parametrize("Hq,Hkv", LAYOUTS)
+@pytest.mark.parametrize("keys", [5, 700])
+def test_the_log_sum_exp_does_not_depend_on_the_values(Hq, Hkv, keys):
+    """Value scales from the least to the largest in one block, in either order, in so many sequences that whole
+    blocks lie on one CTA: no row's log-sum-exp moves by more than rounding (references below 2^8 in size, so
+    2^-16 for each of two, and 2e-5 for the sums)."""
+    m, B = rows_of(Hq, Hkv), 150
+    b = Batch([m] * B, [keys] * B, Hq, Hkv, D, 16, True, seed=keys)
+    plain = np64(call(b.gpu())[1])
+    pages = b.table[:, :-(-min(keys - 1, 300) // 16)].reshape(-1).long()
+    for first, rest in ((17, 240), (240, 17)):
+        b.vs.fill_(rest)
+        b.vs[pages] = first
+        lse = np64(call(b.gpu())[1])
+        fa.check()
+        dead = plain == -np.inf
+        assert np.array_equal(dead, lse == -np.inf), (first, rest)
+        assert np.abs(np.where(dead, 0, lse) - np.where(dead, 0, plain)).max() <= 6e-5, (first, rest)
